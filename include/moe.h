@@ -340,6 +340,147 @@ int moe_mxfp4_pack(const moe_dims* dims, int32_t which, const uint8_t* w, const 
  * its block.  Asynchronous on `stream` like every call. */
 int moe_mx_split(int64_t rows, int32_t cols, const void* x, uint8_t* codes, uint8_t* scales, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Stand-alone operators
+ *
+ * The layer above fixes its products, its activation and its formats.  These
+ * are the same steps taken apart, for blocks that differ (expert biases, other
+ * activations, adapters, fp16, other widths, 4-bit integer weights, the norms
+ * around the block).  They share the layer's conventions: device pointers, the
+ * caller's workspace and stream, validation before the first launch, error
+ * codes, no allocation, no host synchronisation, bitwise-deterministic results
+ * (sums over rows are taken in a fixed order), nothing kept between calls.
+ * Element types: */
+enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 };
+
+/* Grouped matrix products by expert, ragged segments.  Expert e owns the
+ * sorted rows s in [expert_offsets[e], expert_offsets[e+1]); row s reads input
+ * row r(s) = sorted_pairs[s] / k of the T rows of `a`, or, with sorted_pairs
+ * NULL, row s of M rows.  expert_offsets and sorted_pairs are what moe_permute
+ * writes.
+ *   forward  c[s][n]   = sum_k a[r(s)][k] b[e][n][k] + bias[e][n]
+ *   dgrad    da[s][k]  = sum_n dc[s][n] b[e][n][k]          (per sorted row)
+ *   wgrad    db[e][n][k] (+)= sum over e's rows s of dc[s][n] a[r(s)][k]
+ *            dbias[e][n] (+)= sum over e's rows s of dc[s][n]
+ * a: dtype, row stride lda elements (0: K), last index contiguous; da the
+ * same, M rows; c and dc: row stride ldc (0: N); b: [E][N][K] and bias [E][N],
+ * dtype, contiguous; bias may be NULL.  c, da and db have out_dtype: dtype or
+ * MOE_DT_F32; dbias is fp32, or NULL.  Products are exact, sums fp32, each
+ * result rounded once.
+ * accumulate = 1 (wgrad only, out_dtype F32): db and dbias are added to.
+ *
+ * Any N, K >= 1 and any stride; pointers need only their element's alignment.
+ * Rows of a, b and dc whose starts are all 16-byte aligned (K, N where it is
+ * contracted or transposed, strides multiples of 8) take the fast loads.
+ * Segments are read as clamped to [0, M], empty where an offset decreases;
+ * rows outside every segment are left as they were, an expert without rows
+ * gets zero gradients.  A sorted pair outside [0, T * k) reads a row of zeros.
+ * expert_offsets may be NULL when E = 1 (all M rows).  M = 0: forward and
+ * dgrad do nothing, wgrad writes zeros (nothing when accumulating).
+ * Errors: NULL, sizes < 1 (M, T < 0), a stride below the row's length, missing
+ * offsets -> MOE_ERR_INVALID_ARG; E > 256, k > 8, another type, accumulate
+ * elsewhere, N or K > 2^22, sizes beyond one launch's grid ->
+ * MOE_ERR_UNSUPPORTED; outputs must not overlap inputs. */
+typedef struct moe_gmm {
+    int32_t M, N, K, E;
+    int32_t T, k; /* with sorted_pairs: a has T rows, pair p reads row p / k */
+    int32_t dtype, out_dtype;
+    int32_t accumulate;
+    int32_t reserved; /* 0 */
+    int64_t lda, ldc;
+} moe_gmm;
+
+int moe_grouped_mm(const moe_gmm* g, const void* a, const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                   const void* b, const void* bias, void* c, void* stream);
+int moe_grouped_mm_dgrad(const moe_gmm* g, const void* dc, const int32_t* expert_offsets, const void* b, void* da,
+                         void* stream);
+/* Workspace of the weight gradient (16-byte aligned). */
+int moe_grouped_mm_workspace_size(const moe_gmm* g, size_t* bytes);
+int moe_grouped_mm_wgrad(const moe_gmm* g, const void* a, const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                         const void* dc, void* db, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Products with 4-bit integer weights and a scale per group, for few rows per
+ * expert (decoding; any number of rows is right, but the weights are read
+ * again for every 16 rows of an expert):
+ *   w[e][n][i] = scales[e][n][i / group] * (code - zero),
+ *   v[s][n]    = sum_i x[r(s)][i] w[e][n][i] + bias[e][n],
+ *   act NONE:   y[s][n] = v[s][n]                                    y [M][N]
+ *   act SWIGLU: y[s][n] = silu(v[s][n]) * v[s][N/2 + n], n < N/2     y [M][N/2]
+ * codes u8 [E][N][K/2]: element 2b in the low nibble of byte b, as in the
+ * layer's MXFP4 layout, unsigned 0..15; scales [E][N][ceil(K/group)] of dtype;
+ * zeros u8 of the same shape (the low 4 bits are used), or NULL: 8 everywhere.
+ * x [T][K] (sorted_pairs NULL: [M][K]) and bias [E][N] of dtype; y of dtype or
+ * MOE_DT_F32.  group is 32, 64 or 128; the last group of a row may be partial.
+ * code - zero is an exact integer, its products with x are summed in fp32 per
+ * group and scaled in fp32: nothing is rounded before y.
+ * Rows, segments, pairs, E = 1 without offsets: as for moe_grouped_mm.
+ * K must be a multiple of 32, x and codes 16-byte aligned.  Errors as there;
+ * group, K % 32 and type -> MOE_ERR_UNSUPPORTED; an odd N with SWIGLU ->
+ * MOE_ERR_INVALID_ARG. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 };
+typedef struct moe_w4 {
+    int32_t M, N, K, E;
+    int32_t T, k;
+    int32_t group;
+    int32_t dtype, out_dtype;
+    int32_t act;
+} moe_w4;
+
+int moe_w4_matvec(const moe_w4* d, const void* x, const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                  const uint8_t* codes, const void* scales, const uint8_t* zeros, const void* bias, void* y,
+                  void* stream);
+
+/* The norms around a block, with its gate, dropout and scaled residual:
+ *   moe_norm_in    y   = n(x) * weight + bias
+ *   moe_norm_out   out = res_scale * residual + gate * drop(n(f) * weight + bias)
+ * over rows of H, T of them, contiguous, of dtype (bf16, fp16 or fp32);
+ * statistics and arithmetic in fp32, one rounding at the end.
+ *   n(x): MOE_NORM_RMS    x / sqrt(mean(x^2) + eps)
+ *         MOE_NORM_LAYER  (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *         MOE_NORM_NONE   x (moe_norm_out only, weight and bias NULL)
+ * weight, bias [H] of wdtype (dtype or MOE_DT_F32); NULL: 1 and 0.
+ * gate, of dtype: MOE_GATE_CHANNEL [H], MOE_GATE_TOKEN [T], MOE_GATE_FULL
+ * [T][H]; MOE_GATE_NONE: NULL.  residual NULL: none.  out may be the residual's
+ * own buffer, dx that of dres, in every case the same address; otherwise
+ * outputs must not overlap inputs.
+ * drop: with dropout_p > 0, element (t, h) is kept when its 16 random bits are
+ * at least q = round(65536 dropout_p), and then scaled by 65536 / (65536 - q);
+ * a dropped element is 0 whatever its value.  The bits are half (h % 2; low
+ * first) of word h % 8 / 2 of Philox4x32-10 at counter (h / 8, t, offset low
+ * word, offset high word) with key seed; rng points to {seed, offset} in device
+ * memory, so a captured graph draws a new mask when they are updated.  The mask
+ * is never stored: the backward draws it again from the same {seed, offset}.
+ * H <= 16384.  Pointers need their element's alignment.  T = 0: nothing is
+ * computed, sums over rows are zero.
+ *
+ * Backward of moe_norm_in for the gradient dy of y; dres, if not NULL, is the
+ * gradient of the residual stream behind the block, which passes it scaled:
+ *   dx = (gradient through the norm) + res_scale * dres.
+ * Backward of moe_norm_out for the gradient dout of out: df, and dgate in the
+ * gate's shape, fp32 for CHANNEL and TOKEN, dtype for FULL.  (The residual's
+ * gradient is res_scale * dout; moe_norm_in_backward adds it.)
+ * dweight, dbias fp32 [H]; these and dgate may be NULL.  The statistics are
+ * taken again from x or f.  Workspace: moe_norm_workspace_size bytes, 16-byte
+ * aligned, the same for both. */
+enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+typedef struct moe_norm {
+    int32_t T, H;
+    int32_t dtype, wdtype;
+    int32_t kind, gate;
+    float eps, res_scale, dropout_p;
+} moe_norm;
+
+int moe_norm_in(const moe_norm* d, const void* x, const void* weight, const void* bias, void* y, void* stream);
+int moe_norm_out(const moe_norm* d, const void* f, const void* residual, const void* weight, const void* bias,
+                 const void* gate, const uint64_t* rng, void* out, void* stream);
+int moe_norm_workspace_size(const moe_norm* d, size_t* bytes);
+int moe_norm_in_backward(const moe_norm* d, const void* x, const void* weight, const void* dy, const void* dres,
+                         void* dx, float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+int moe_norm_out_backward(const moe_norm* d, const void* f, const void* weight, const void* bias, const void* gate,
+                          const uint64_t* rng, const void* dout, void* df, float* dweight, float* dbias, void* dgate,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for an error code. */
 const char* moe_strerror(int code);
 

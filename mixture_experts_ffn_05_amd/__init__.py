@@ -20,12 +20,18 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_MISALIGNED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(6)
 MOE_WFMT_BF16, MOE_WFMT_MXFP4, MOE_WFMT_MXFP4_PACKED = 0, 1, 2
 MOE_PACK_GATE_UP, MOE_PACK_DOWN = 0, 1
+MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32 = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 MOE_PATH_AUTO, MOE_PATH_SKINNY, MOE_PATH_TILED, MOE_PATH_TILED_DEQUANT, MOE_PATH_TILED_MX = 0, 1, 2, 3, 4
 
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_permute", "moe_gate_up", "moe_down", "moe_grouped_ffn",
             "moe_combine", "moe_forward", "moe_forward_noalloc", "moe_backward_workspace_size", "moe_backward",
             "moe_mxfp4_quantize", "moe_mxfp4_fakequant", "moe_mxfp4_pack", "moe_mx_split", "moe_strerror",
-            "moe_last_error")
+            "moe_last_error", "moe_grouped_mm", "moe_grouped_mm_dgrad", "moe_grouped_mm_workspace_size",
+            "moe_grouped_mm_wgrad", "moe_w4_matvec", "moe_norm_in", "moe_norm_out", "moe_norm_workspace_size",
+            "moe_norm_in_backward", "moe_norm_out_backward")
 
 
 class MoeLibraryMissing(RuntimeError):
@@ -48,6 +54,20 @@ class moe_expert_weights(ctypes.Structure):
                 ("down_scale", ctypes.c_void_p)]
 
 
+class moe_gmm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "E", "T", "k", "dtype", "out_dtype", "accumulate",
+                                              "reserved")] + [("lda", ctypes.c_int64), ("ldc", ctypes.c_int64)]
+
+
+class moe_w4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "E", "T", "k", "group", "dtype", "out_dtype", "act")]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "wdtype", "kind", "gate")] + \
+               [(n, ctypes.c_float) for n in ("eps", "res_scale", "dropout_p")]
+
+
 _lib = None
 
 
@@ -65,6 +85,7 @@ def library(path: str | None = None):
     lib = ctypes.CDLL(p)
     V, I32, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     D, W = ctypes.POINTER(moe_dims), ctypes.POINTER(moe_expert_weights)
+    G, N = ctypes.POINTER(moe_gmm), ctypes.POINTER(moe_norm)
     sig = {
         "moe_workspace_size": [D, ctypes.POINTER(SZ)],
         "moe_route": [D, V, V, V, V, V, SZ, V],
@@ -81,6 +102,16 @@ def library(path: str | None = None):
         "moe_mxfp4_fakequant": [ctypes.c_int64, ctypes.c_int32, V, V, V],
         "moe_mxfp4_pack": [D, ctypes.c_int32, V, V, V, V, V],
         "moe_mx_split": [ctypes.c_int64, ctypes.c_int32, V, V, V, V],
+        "moe_grouped_mm": [G, V, V, V, V, V, V, V],
+        "moe_grouped_mm_dgrad": [G, V, V, V, V, V],
+        "moe_grouped_mm_workspace_size": [G, ctypes.POINTER(SZ)],
+        "moe_grouped_mm_wgrad": [G, V, V, V, V, V, V, V, SZ, V],
+        "moe_w4_matvec": [ctypes.POINTER(moe_w4), V, V, V, V, V, V, V, V, V],
+        "moe_norm_in": [N, V, V, V, V, V],
+        "moe_norm_out": [N, V, V, V, V, V, V, V, V],
+        "moe_norm_workspace_size": [N, ctypes.POINTER(SZ)],
+        "moe_norm_in_backward": [N, V, V, V, V, V, V, V, V, SZ, V],
+        "moe_norm_out_backward": [N, V, V, V, V, V, V, V, V, V, V, V, SZ, V],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -218,9 +249,120 @@ def moe_mx_split(rows: int, cols: int, x, codes, scales, stream=None):
     _check("moe_mx_split", library().moe_mx_split(rows, cols, _ptr(x), _ptr(codes), _ptr(scales), _stream(stream)))
 
 
+# --------------------------------------------------------------------- stand-alone operators
+
+
+class _DTypes:
+    """torch dtype -> MOE_DT_*."""
+
+    def __getitem__(self, dtype):
+        import torch
+        return {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}[dtype]
+
+
+DTYPE = _DTypes()
+
+
+def _on_device(*tensors):
+    """The stream the call goes to by default is the current device's: refuse
+    tensors that live elsewhere (they would be reached, if at all, over a link
+    and without ordering)."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda or (cur is not None and t.get_device() != cur):
+            raise ValueError(f"tensor on {t.device} while the current device is cuda:{cur}")
+
+
+def gmm(M: int, N: int, K: int, E: int, T: int = 0, k: int = 1, dtype: int = MOE_DT_BF16, out_dtype: int | None = None,
+        accumulate: bool = False, lda: int = 0, ldc: int = 0) -> moe_gmm:
+    return moe_gmm(M, N, K, E, T, k, dtype, dtype if out_dtype is None else out_dtype, int(accumulate), 0, lda, ldc)
+
+
+def w4(M: int, N: int, K: int, E: int, T: int = 0, k: int = 1, group: int = 128, dtype: int = MOE_DT_BF16,
+       out_dtype: int | None = None, act: int = MOE_ACT_NONE) -> moe_w4:
+    return moe_w4(M, N, K, E, T, k, group, dtype, dtype if out_dtype is None else out_dtype, act)
+
+
+def norm(T: int, H: int, dtype: int = MOE_DT_BF16, wdtype: int | None = None, kind: int = MOE_NORM_RMS,
+         eps: float = 1e-5, gate: int = MOE_GATE_NONE, res_scale: float = 1.0, dropout_p: float = 0.0) -> moe_norm:
+    return moe_norm(T, H, dtype, dtype if wdtype is None else wdtype, kind, gate, eps, res_scale, dropout_p)
+
+
+def moe_grouped_mm(g, a, expert_offsets, sorted_pairs, b, bias, c, stream=None):
+    _on_device(a, expert_offsets, sorted_pairs, b, bias, c)
+    _check("moe_grouped_mm", library().moe_grouped_mm(ctypes.byref(g), _ptr(a), _ptr(expert_offsets),
+                                                     _ptr(sorted_pairs), _ptr(b), _ptr(bias), _ptr(c),
+                                                     _stream(stream)))
+
+
+def moe_grouped_mm_dgrad(g, dc, expert_offsets, b, da, stream=None):
+    _on_device(dc, expert_offsets, b, da)
+    _check("moe_grouped_mm_dgrad", library().moe_grouped_mm_dgrad(ctypes.byref(g), _ptr(dc), _ptr(expert_offsets),
+                                                                 _ptr(b), _ptr(da), _stream(stream)))
+
+
+def moe_grouped_mm_workspace_size(g) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_grouped_mm_workspace_size", library().moe_grouped_mm_workspace_size(ctypes.byref(g), ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_mm_wgrad(g, a, expert_offsets, sorted_pairs, dc, db, dbias, ws, ws_bytes, stream=None):
+    _on_device(a, expert_offsets, sorted_pairs, dc, db, dbias, ws)
+    _check("moe_grouped_mm_wgrad", library().moe_grouped_mm_wgrad(ctypes.byref(g), _ptr(a), _ptr(expert_offsets),
+                                                                 _ptr(sorted_pairs), _ptr(dc), _ptr(db), _ptr(dbias),
+                                                                 _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_w4_matvec(d, x, expert_offsets, sorted_pairs, codes, scales, zeros, bias, y, stream=None):
+    _on_device(x, expert_offsets, sorted_pairs, codes, scales, zeros, bias, y)
+    _check("moe_w4_matvec", library().moe_w4_matvec(ctypes.byref(d), _ptr(x), _ptr(expert_offsets), _ptr(sorted_pairs),
+                                                   _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(y),
+                                                   _stream(stream)))
+
+
+def moe_norm_in(d, x, weight, bias, y, stream=None):
+    _on_device(x, weight, bias, y)
+    _check("moe_norm_in", library().moe_norm_in(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                               _stream(stream)))
+
+
+def moe_norm_out(d, f, residual, weight, bias, gate, rng, out, stream=None):
+    _on_device(f, residual, weight, bias, gate, rng, out)
+    _check("moe_norm_out", library().moe_norm_out(ctypes.byref(d), _ptr(f), _ptr(residual), _ptr(weight), _ptr(bias),
+                                                 _ptr(gate), _ptr(rng), _ptr(out), _stream(stream)))
+
+
+def moe_norm_workspace_size(d) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_norm_workspace_size", library().moe_norm_workspace_size(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def moe_norm_in_backward(d, x, weight, dy, dres, dx, dweight, dbias, ws, ws_bytes, stream=None):
+    _on_device(x, weight, dy, dres, dx, dweight, dbias, ws)
+    _check("moe_norm_in_backward", library().moe_norm_in_backward(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(dy),
+                                                                 _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                                                 _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def moe_norm_out_backward(d, f, weight, bias, gate, rng, dout, df, dweight, dbias, dgate, ws, ws_bytes, stream=None):
+    _on_device(f, weight, bias, gate, rng, dout, df, dweight, dbias, dgate, ws)
+    _check("moe_norm_out_backward", library().moe_norm_out_backward(ctypes.byref(d), _ptr(f), _ptr(weight), _ptr(bias),
+                                                                   _ptr(gate), _ptr(rng), _ptr(dout), _ptr(df),
+                                                                   _ptr(dweight), _ptr(dbias), _ptr(dgate), _ptr(ws),
+                                                                   ws_bytes, _stream(stream)))
+
+
 __all__ = ["library", "dims", "expert_weights", "strerror", "moe_workspace_size", "moe_route", "moe_permute",
            "moe_gate_up", "moe_down", "moe_grouped_ffn", "moe_combine", "moe_forward", "moe_forward_noalloc",
            "MOE_NOALLOC_SCRATCH_BYTES", "moe_backward_workspace_size",
            "moe_backward", "moe_mxfp4_quantize",
            "moe_mxfp4_fakequant", "moe_mxfp4_pack", "moe_mx_split", "moe_dims",
-           "moe_expert_weights", "MoeError", "MoeLibraryMissing", "EXPORTED", "LIB_PATH"]
+           "moe_expert_weights", "moe_gmm", "moe_w4", "moe_norm", "gmm", "w4", "norm", "DTYPE", "moe_grouped_mm",
+           "moe_grouped_mm_dgrad", "moe_grouped_mm_workspace_size", "moe_grouped_mm_wgrad", "moe_w4_matvec",
+           "moe_norm_in", "moe_norm_out", "moe_norm_workspace_size", "moe_norm_in_backward", "moe_norm_out_backward",
+           "MoeError", "MoeLibraryMissing", "EXPORTED", "LIB_PATH"]

@@ -1,0 +1,791 @@
+// Grouped matrix products by expert, ragged segments, and their gradients.
+//
+// Expert e owns the sorted rows [offsets[e], offsets[e+1]); row s reads input
+// row r(s) = pairs[s] / k (or s).  The three products
+//   forward   c[s][n]    = sum_k a[r(s)][k] b[e][n][k] + bias[e][n]
+//   dgrad     da[s][k]   = sum_n dc[s][n] b[e][n][k]
+//   wgrad     db[e][n][k] (+)= sum_{s in e} dc[s][n] a[r(s)][k]
+// are one tiled kernel, D[r][c] = sum_j P[r][j] Q[c][j] per tile, on
+// v_mfma_f32_32x32x16_{bf16,f16} with fp32 accumulation:
+//   forward: P = weight rows n,         Q = token rows s,      j = k
+//   dgrad:   P = weight columns k,      Q = rows of dc,        j = n
+//   wgrad:   P = columns k of a,        Q = columns n of dc,   j = the segment's rows
+// P's index is the output's contiguous one in all three, so a lane's four
+// consecutive accumulator rows are one vector store.
+//
+// Operands whose memory is contiguous along j are staged as [rows][32 j] LDS
+// tiles.  Operands contiguous along r or c (the weights of dgrad, both
+// operands of wgrad) are staged as they lie, [32 j][columns], and
+// ds_read_b64_tr_b16 transposes them on the way to the registers: no
+// transposed copy of the weights or of the activations is ever written.
+// Both kinds give a lane the j values 16 s + 8 (lane / 32) + 0..7 in order, so
+// either kind can meet either in one MFMA.
+//
+// The tile loop is a ring of 4 LDS stages of 32 j: direct-to-LDS loads run
+// three stages ahead, one barrier a stage, placed after the first half of the
+// stage's MFMAs.  Loads past the contracted length, and past the matrix's
+// width in a transposed tile, read a 16-byte block of zeros, so tails cost no
+// branch and no garbage enters a product.  Rows and widths that are not
+// multiples of 8 elements (or bases not 16-byte aligned) cannot use the
+// direct loads (VEC = false): they go through registers, two stages ahead,
+// with unaligned 16-byte loads and an element loop only in a row's last chunk.
+#include <string.h>
+
+#include <type_traits>
+#include <utility>
+
+#include "elem16.h"
+#include "moe_ops.h"
+#include "tile_sched.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int GP_BK = 32;
+constexpr int GP_NBUF = 4;
+
+enum { GP_FWD = 0, GP_DGRAD = 1, GP_WGRAD = 2 };
+
+// Tile shapes: WR x WC waves, each WB x TB blocks of 32 x 32.
+template <int WR_, int WC_, int WB_, int TB_>
+struct TileCfg {
+    static constexpr int WR = WR_, WC = WC_, WB = WB_, TB = TB_;
+    static constexpr int NW = WR * WC, THREADS = NW * WAVE;
+    static constexpr int BR = WR * WB * 32, BC = WC * TB * 32;
+};
+using TileLarge = TileCfg<2, 4, 4, 2>;  // 256 x 256, 8 waves
+using TileSmall = TileCfg<2, 2, 2, 1>;  // 128 x 64, 4 waves
+
+__device__ uint32_t gp_zeros[4] __attribute__((aligned(16)));  // never written
+
+struct GpArgs {
+    int M, N, K, E, a_rows;
+    unsigned long long k_magic;  // p / k = (p * k_magic) >> k_shift for 0 <= p < 2^31
+    int k_shift;
+    long long lda, ldc;
+    const int32_t* offsets;
+    const int32_t* pairs;
+    const void* a;
+    const void* b;
+    const void* bias;
+    const void* dc;
+    void* out;
+    int splits;
+    int accumulate;
+};
+
+// Input row of sorted position s; a pair outside [0, a_rows * k) gives -1 (a
+// row of zeros).
+__device__ __forceinline__ int input_row(const GpArgs& g, int p)
+{
+    const int r = (int)(((unsigned long long)(unsigned)p * g.k_magic) >> g.k_shift);
+    return ((p >= 0) & (r < g.a_rows)) ? r : -1;
+}
+
+// M-tile `tile` of the schedule in which expert e owns ceil(len_e / BC) * nt
+// consecutive tiles; every wave computes the same.  Also returns the number of
+// tiles of all experts.
+template <int BC>
+__device__ __forceinline__ int gp_total(const GpArgs& g, int nt)
+{
+    int n = 0;
+    for (int base = 0; base < g.E; base += WAVE) {
+        const int e = base + lane_id();
+        int mt = 0;
+        if (e < g.E) {
+            const Segment sg = segment_of(g.offsets, e, g.M);
+            mt = (sg.end - sg.begin + BC - 1) / BC;
+        }
+        n += wave_sum(mt);
+    }
+    return n * nt;
+}
+
+template <int BC>
+__device__ __forceinline__ int gp_locate(const GpArgs& g, int nt, int tile, int* local, int* mtiles)
+{
+    const int lane = lane_id();
+    int before = 0;
+    for (int base = 0; base < g.E; base += WAVE) {
+        const int e = base + lane;
+        int mt = 0;
+        if (e < g.E) {
+            const Segment sg = segment_of(g.offsets, e, g.M);
+            mt = (sg.end - sg.begin + BC - 1) / BC;
+        }
+        const int n = mt * nt;
+        const int excl = wave_excl_scan(n) + before;
+        const uint64_t hm = ballot(n > 0 && tile >= excl && tile < excl + n);
+        if (hm) {
+            const int src = (int)__builtin_ctzll(hm);
+            *local = tile - __shfl(excl, src, WAVE);
+            *mtiles = __shfl(mt, src, WAVE);
+            return base + src;
+        }
+        before = __shfl(excl + n, WAVE - 1, WAVE);
+    }
+    return -1;
+}
+
+// The expert whose segment has rank `rank` by descending length (ties: lower
+// index first).  E <= 256: lane l holds experts l, l + 64, ...
+__device__ __forceinline__ int gp_ranked_expert(const GpArgs& g, int rank)
+{
+    const int lane = lane_id();
+    int len[4], rk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = lane + WAVE * i;
+        len[i] = -1;
+        rk[i] = 0;
+        if (e < g.E) {
+            const Segment sg = segment_of(g.offsets, e, g.M);
+            len[i] = sg.end - sg.begin;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (WAVE * j >= g.E) break;  // uniform
+        for (int o = 0; o < min(WAVE, g.E - WAVE * j); ++o) {
+            const int lo = __builtin_amdgcn_readlane(len[j], o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                rk[i] += (lo > len[i] || (lo == len[i] && WAVE * j + o < lane + WAVE * i)) ? 1 : 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t hit = ballot(lane + WAVE * i < g.E && rk[i] == rank);
+        if (hit) return WAVE * i + (int)__builtin_ctzll(hit);
+    }
+    return -1;
+}
+
+typedef __attribute__((address_space(4))) const int32_t* gp_cptr;  // read through the scalar unit
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((address_space(3))) s16x4* gp_trptr;
+
+// 8 elements from p on; those from element `left` on are 0.  p may be the
+// 16-byte block of zeros.
+template <typename T>
+__device__ __forceinline__ u32x4 load8_masked(const T* p, const T* zeros, int left)
+{
+    if (left >= 8 || p == zeros) return load16_any(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) w[i >> 1] |= (uint32_t)p[i].v << (16 * (i & 1));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+// Order in which a half stage's NR LDS reads and NM MFMAs are issued: the
+// reads spread evenly among the MFMAs.
+template <int NR, int NM, int... I>
+__device__ __forceinline__ void gp_interleave(std::integer_sequence<int, I...>)
+{
+    (
+        [] {
+            constexpr int reads = NR * (I + 1) / NM - NR * I / NM;
+            if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }(),
+        ...);
+}
+
+// GATHER (wgrad): rows of a through pairs.  The forward gathers by `pairs`
+// itself, once per tile.
+template <typename T, typename O, int MODE, bool VEC, bool GATHER, typename Cfg>
+__global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(GpArgs g)
+{
+    constexpr int BR = Cfg::BR, BC = Cfg::BC, NW = Cfg::NW, WB = Cfg::WB, TB = Cfg::TB;
+    constexpr bool P_TR = MODE != GP_FWD, Q_TR = MODE == GP_WGRAD;
+    constexpr int DLP = BR * 64 / 1024 / NW, DLQ = BC * 64 / 1024 / NW;  // 1 KB loads per wave per stage
+    constexpr int L = DLP + DLQ;
+    static_assert(DLP >= 1 && DLQ >= 1, "a stage is whole loads");
+    __shared__ __attribute__((aligned(16))) uint8_t shp[GP_NBUF][BR * 64];
+    __shared__ __attribute__((aligned(16))) uint8_t shq[GP_NBUF][BC * 64];
+
+    const int R = MODE == GP_FWD ? g.N : g.K;  // the tile's row index runs over these
+    const int nt = (R + BR - 1) / BR;
+
+    // ---- tile of this block (uniform per block)
+    int e, local, mtiles, split = 0;
+    if constexpr (MODE == GP_WGRAD) {
+        // An expert's tiles all contract over its own number of rows, so the
+        // experts go out longest first; within an expert every XCD (blocks are
+        // dealt round-robin over the 8) takes one contiguous run of the banded
+        // tile order and shares its operand strips in its L2.
+        mtiles = (g.N + BC - 1) / BC;
+        const int tpe = mtiles * nt, tpe8 = (tpe + 7) / 8 * 8;
+        const int t = (int)(blockIdx.x % tpe8);
+        const int er = (int)(blockIdx.x / tpe8);
+        local = (t % 8) * (tpe8 / 8) + t / 8;
+        if (local >= tpe) return;
+        split = er % g.splits;
+        e = gp_ranked_expert(g, er / g.splits);
+        if (e < 0) return;
+    } else {
+        const int total = gp_total<BC>(g, nt);
+        const int per = (total + 7) / 8;
+        if ((int)(blockIdx.x / 8) >= per) return;
+        const int tile = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+        if (tile >= total) return;
+        e = gp_locate<BC>(g, nt, tile, &local, &mtiles);
+        if (e < 0) return;
+    }
+    int mt, ntile;
+    gm_band(local, mtiles, nt, &mt, &ntile);
+    const int r0 = ntile * BR;
+    const Segment seg = segment_of(g.offsets, e, g.M);
+    int J;       // contracted length
+    int c0, c1;  // the tile's first column-role index and the end of its range
+    int j0 = 0;  // WGRAD: first row of the split, relative to the segment
+    if constexpr (MODE == GP_WGRAD) {
+        const int len = seg.end - seg.begin;
+        const int per = ((len + g.splits - 1) / g.splits + GP_BK - 1) / GP_BK * GP_BK;
+        j0 = min(split * per, len);
+        J = min(per, len - j0);
+        c0 = mt * BC;
+        c1 = g.N;
+    } else {
+        J = MODE == GP_FWD ? g.K : g.N;
+        c0 = seg.begin + mt * BC;
+        c1 = seg.end;
+    }
+    const int nstages = (J + GP_BK - 1) / GP_BK;
+
+    const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
+    // Waves w and w + 4 share a SIMD: they take column parts half a tile apart,
+    // so that a tile with few valid columns keeps every SIMD busy.  A wave
+    // without valid rows or columns still stages its share and meets every barrier.
+    const int wr = wave / Cfg::WC, wc = (wave + (Cfg::WC / 2) * wr) % Cfg::WC;
+    const bool live = c0 + 32 * TB * wc < c1 && r0 + 32 * WB * wr < R;
+
+    // ---- sources of this wave's 1 KB loads.  Contiguous along j: load i covers
+    // tile rows 16 (wave + NW i) + lane / 4, lane l landing in 16-byte slot l %
+    // 4 of its row, which holds logical chunk (l % 4) ^ (row / 4 % 4).
+    // Transposed: tile rows are j; a row of RB bytes holds its 64-byte segments
+    // XORed with tr_xor(row), so that the four rows one transposing read
+    // touches fall on different banks.
+    const T* zeros = reinterpret_cast<const T*>(gp_zeros);
+    auto tr_xor = [](int row, int RB) { return RB >= 256 ? row & 3 : (row >> 1) & 1; };
+    constexpr int PRB = BR * 2, QRB = BC * 2;
+    constexpr int PRPL = 1024 / PRB, QRPL = 1024 / QRB;  // rows per load of a transposed tile
+
+    const T* psrc[DLP];  // row base (contiguous) or column base of row 0 (transposed)
+    const T* qsrc[DLQ];
+    int pj[DLP], qj[DLQ];  // contiguous: first j of the lane's chunk; transposed: its row
+    int plim[DLP], qlim[DLQ];  // end of the valid j; 0: no valid element at all
+    int pcol[DLP] = {}, qcol[DLQ] = {};  // transposed: first column
+    const T* A = static_cast<const T*>(g.a);
+    const T* B = static_cast<const T*>(g.b) + (size_t)e * g.N * g.K;
+    const T* DC = static_cast<const T*>(g.dc);
+#pragma unroll
+    for (int i = 0; i < DLP; ++i) {
+        if constexpr (!P_TR) {
+            const int row = 16 * (wave + NW * i) + (lane >> 2);
+            pj[i] = 8 * ((lane & 3) ^ ((row >> 2) & 3));
+            const bool ok = r0 + row < R;
+            plim[i] = ok ? J : 0;
+            psrc[i] = ok ? B + (size_t)(r0 + row) * g.K : zeros;
+        } else {
+            const int row = PRPL * (wave + NW * i) + lane / (WAVE / PRPL), p = lane % (WAVE / PRPL);
+            pj[i] = row;
+            pcol[i] = r0 + 8 * ((((p >> 2) ^ tr_xor(row, PRB)) << 2) | (p & 3));
+            plim[i] = pcol[i] < R ? J : 0;
+            psrc[i] = (MODE == GP_DGRAD ? B : A) + (pcol[i] < R ? pcol[i] : 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < DLQ; ++i) {
+        if constexpr (!Q_TR) {
+            const int row = 16 * (wave + NW * i) + (lane >> 2);
+            const int s = c0 + row;
+            qj[i] = 8 * ((lane & 3) ^ ((row >> 2) & 3));
+            bool ok = s < c1;
+            int r = s;
+            if constexpr (MODE == GP_FWD) {
+                if (ok && g.pairs) r = input_row(g, g.pairs[s]);
+                ok = ok && (unsigned)r < (unsigned)g.a_rows;
+            }
+            qlim[i] = ok ? J : 0;
+            qsrc[i] = (MODE == GP_FWD ? A : DC) + (ok ? (size_t)r * (MODE == GP_FWD ? g.lda : g.ldc) : 0);
+        } else {
+            const int row = QRPL * (wave + NW * i) + lane / (WAVE / QRPL), p = lane % (WAVE / QRPL);
+            qj[i] = row;
+            qcol[i] = c0 + 8 * ((((p >> 2) ^ tr_xor(row, QRB)) << 2) | (p & 3));
+            qlim[i] = qcol[i] < c1 ? J : 0;
+            qsrc[i] = DC + (qcol[i] < c1 ? qcol[i] : 0);
+        }
+    }
+    // WGRAD with gathered rows: the pair ids of the next stage's rows, read
+    // one stage early through the scalar unit (vector loads would have to be
+    // waited for in order with the tiles in flight).
+    [[maybe_unused]] int prow[DLP][PRPL];
+    auto load_rows = [&](int st) {
+        if constexpr (GATHER) {
+            gp_cptr ids = (gp_cptr)(uintptr_t)g.pairs;
+#pragma unroll
+            for (int i = 0; i < DLP; ++i) {
+                const int first = __builtin_amdgcn_readfirstlane(st * GP_BK + PRPL * (wave + NW * i));
+#pragma unroll
+                for (int q = 0; q < PRPL; ++q) prow[i][q] = ids[seg.begin + j0 + min(first + q, J - 1)];
+            }
+        }
+    };
+    // Source address of load i at stage st; the zeros past the operand's end.
+    // Branch-free: a branch here makes the compiler wait for every load in
+    // flight at the join.
+    auto pick = [&](bool ok, const T* src) {
+        return reinterpret_cast<const T*>(ok ? reinterpret_cast<uintptr_t>(src) : reinterpret_cast<uintptr_t>(zeros));
+    };
+    auto p_ok = [&](int i, int st) { return st * GP_BK + pj[i] < plim[i]; };
+    auto q_ok = [&](int i, int st) { return st * GP_BK + qj[i] < qlim[i]; };
+    auto p_at = [&](int i, int st) -> const T* {
+        const int j = st * GP_BK + pj[i];
+        if constexpr (!P_TR) {
+            return pick(p_ok(i, st), psrc[i] + j);
+        } else if constexpr (MODE == GP_DGRAD) {
+            return pick(p_ok(i, st), psrc[i] + (size_t)(unsigned)j * (unsigned)g.K);
+        } else {
+            int r = seg.begin + j0 + j;
+            if constexpr (GATHER) {
+                const int sub = lane / (WAVE / PRPL);
+                int p = prow[i][0];
+#pragma unroll
+                for (int q = 1; q < PRPL; ++q) p = sub == q ? prow[i][q] : p;
+                r = input_row(g, p);
+            }
+            return pick(p_ok(i, st) & ((unsigned)r < (unsigned)g.a_rows), psrc[i] + (long long)r * g.lda);
+        }
+    };
+    auto q_at = [&](int i, int st) -> const T* {
+        const int j = st * GP_BK + qj[i];
+        if constexpr (!Q_TR)
+            return pick(q_ok(i, st), qsrc[i] + j);
+        else
+            return pick(q_ok(i, st), qsrc[i] + (long long)(seg.begin + j0 + j) * g.ldc);
+    };
+
+    // ---- VEC: direct-to-LDS loads of stage st
+    auto issue = [&](int st) {
+        const int buf = st % GP_NBUF;
+#pragma unroll
+        for (int i = 0; i < DLP; ++i) {
+            dma16(p_at(i, st), shp[buf] + 1024 * (wave + NW * i));
+        }
+#pragma unroll
+        for (int i = 0; i < DLQ; ++i) {
+            dma16(q_at(i, st), shq[buf] + 1024 * (wave + NW * i));
+        }
+        load_rows(st + 1);
+    };
+    // ---- otherwise: through registers
+    [[maybe_unused]] u32x4 rp[2][DLP], rq[2][DLQ];
+    auto fetch = [&](int set, int st) {
+        const u32x4 z = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < DLP; ++i) {
+            const int left = P_TR ? R - pcol[i] : J - (st * GP_BK + pj[i]);
+            rp[set][i] = p_ok(i, st) ? load8_masked(p_at(i, st), zeros, left) : z;
+        }
+#pragma unroll
+        for (int i = 0; i < DLQ; ++i) {
+            const int left = Q_TR ? c1 - qcol[i] : J - (st * GP_BK + qj[i]);
+            rq[set][i] = q_ok(i, st) ? load8_masked(q_at(i, st), zeros, left) : z;
+        }
+        load_rows(st + 1);
+    };
+    auto store = [&](int set, int st) {
+        const int buf = st % GP_NBUF;
+#pragma unroll
+        for (int i = 0; i < DLP; ++i)
+            *reinterpret_cast<u32x4*>(shp[buf] + 1024 * (wave + NW * i) + 16 * lane) = rp[set][i];
+#pragma unroll
+        for (int i = 0; i < DLQ; ++i)
+            *reinterpret_cast<u32x4*>(shq[buf] + 1024 * (wave + NW * i) + 16 * lane) = rq[set][i];
+    };
+
+    f32x16_t acc[WB][TB];
+#pragma unroll
+    for (int m = 0; m < WB; ++m)
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[m][t] = f32x16_t{};
+
+    // ---- operand fragments of one 16-wide j step
+    struct Frags {
+        u32x4 p[WB], q[TB];
+    };
+    const int r32 = lane & 31, kg = lane >> 5;
+    // Transposing read: lane l addresses row l % 16 / 4 (+ 8 for the upper half
+    // wave) and columns 16 (l / 16 % 2) + 4 (l % 4) .. +3 of a 32-column block,
+    // and receives four rows of its own column.
+    const int tr_row = ((lane & 15) >> 2) + 8 * kg;
+    const int tr_in = 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+    auto read_tr = [&](const uint8_t* tile, int RB, int block, int s) {
+        const int seg64 = block ^ tr_xor(tr_row, RB);
+        const uint8_t* at = tile + (tr_row + 16 * s) * RB + seg64 * 64 + tr_in;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gp_trptr)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gp_trptr)(at + 4 * RB));
+        const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
+        return u32x4{l2.x, l2.y, h2.x, h2.y};
+    };
+    auto read_row = [&](const uint8_t* tile, int row, int s) {
+        const int c = (2 * s + kg) ^ ((row >> 2) & 3);
+        return *reinterpret_cast<const u32x4*>(tile + row * 64 + c * 16);
+    };
+    auto load_frags = [&](int buf, int s, Frags& f) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            if constexpr (Q_TR)
+                f.q[t] = read_tr(shq[buf], QRB, TB * wc + t, s);
+            else
+                f.q[t] = read_row(shq[buf], 32 * (TB * wc + t) + r32, s);
+        }
+#pragma unroll
+        for (int m = 0; m < WB; ++m) {
+            if constexpr (P_TR)
+                f.p[m] = read_tr(shp[buf], PRB, WB * wr + m, s);
+            else
+                f.p[m] = read_row(shp[buf], 32 * (WB * wr + m) + r32, s);
+        }
+    };
+    auto mma = [&](const Frags& f) {
+#pragma unroll
+        for (int m = 0; m < WB; ++m)
+#pragma unroll
+            for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(f.p[m], f.q[t], acc[m][t], T{});
+    };
+    constexpr int NR = WB * (P_TR ? 2 : 1) + TB * (Q_TR ? 2 : 1), NM = WB * TB;
+    auto interleave = [&]() { gp_interleave<NR, NM>(std::make_integer_sequence<int, NM>{}); };
+
+    // ---- software pipeline: each stage is two 16-wide steps; the barrier that
+    // publishes stage st+1 sits between them.
+    if (nstages > 0) {
+        load_rows(0);
+        if constexpr (VEC) {
+            for (int st = 0; st < 3; ++st) issue(st);
+            dma_wait<0>();
+        } else {
+            fetch(0, 0);
+            fetch(1, 1);
+            store(0, 0);
+            store(1, 1);
+            fetch(0, 2);
+            fetch(1, 3);
+        }
+        lds_barrier();
+        Frags f0, f1;
+        if (live) load_frags(0, 0, f0);
+        auto stage = [&](int st, auto set_c) {  // set_c = st & 1, a constant so that the sets stay in registers
+            constexpr int SET = decltype(set_c)::value;
+            const int buf = st % GP_NBUF, nb = (st + 1) % GP_NBUF;
+            __builtin_amdgcn_sched_barrier(0);
+            if (live) {
+                load_frags(buf, 1, f1);
+                mma(f0);
+                interleave();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (VEC) dma_wait<L>();  // stage st+1 has landed; st+2's loads may be in flight
+            lds_barrier();                    // stage st+1 visible; the buffer of stage st-1 is free
+            if constexpr (VEC) {
+                issue(st + 3);
+            } else {
+                store(SET, st + 2);
+                fetch(SET, st + 4);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (live) {
+                load_frags(nb, 0, f0);
+                mma(f1);
+                interleave();
+            }
+        };
+        int st = 0;
+        for (; st + 2 < nstages; st += 2) {
+            stage(st, std::integral_constant<int, 0>{});
+            stage(st + 1, std::integral_constant<int, 1>{});
+        }
+        if (st + 1 < nstages) {
+            stage(st, std::integral_constant<int, 0>{});
+            ++st;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (live) {
+            load_frags(st % GP_NBUF, 1, f1);
+            mma(f0);
+            interleave();
+            mma(f1);
+        }
+        mfma_drain();
+        dma_wait<0>();  // the surplus loads past the last stage
+    }
+    if (!live) return;
+
+    // ---- epilogue: block (m, t) of the lane holds tile rows 32 (WB wr + m) +
+    // 8 q + 4 (lane / 32) + 0..3 (q = 0..3) of column 32 (TB wc + t) + lane % 32.
+    O* out;
+    long long ldo;
+    if constexpr (MODE == GP_WGRAD) {
+        out = static_cast<O*>(g.out) + ((size_t)split * g.E + e) * g.N * g.K;
+        ldo = g.K;
+    } else {
+        out = static_cast<O*>(g.out);
+        ldo = MODE == GP_FWD ? g.ldc : g.lda;
+    }
+    const T* bias = MODE == GP_FWD && g.bias ? static_cast<const T*>(g.bias) + (size_t)e * g.N : nullptr;
+#pragma unroll
+    for (int m = 0; m < WB; ++m) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = r0 + 32 * (WB * wr + m) + 8 * q + 4 * kg;
+            if (row >= R) continue;
+            const int nv = min(4, R - row);
+            float bv[4] = {0.f, 0.f, 0.f, 0.f};
+            if (MODE == GP_FWD && bias) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < nv) bv[i] = to_f32(bias[row + i]);
+            }
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                const int c = c0 + 32 * (TB * wc + t) + r32;
+                if (c >= c1) continue;
+                O* at = out + (size_t)c * ldo + row;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = acc[m][t][4 * q + i] + bv[i];
+                if constexpr (std::is_same<O, float>::value) {
+                    if (MODE == GP_WGRAD && g.accumulate) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < nv) v[i] += at[i];
+                    }
+                    if (nv == 4) {
+                        store16_any(at, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                              __float_as_uint(v[3])});
+                        continue;
+                    }
+                } else if (nv == 4) {
+                    store8_any(at, pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3]));
+                    continue;
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (i < nv) at[i] = from_f32<O>(v[i]);
+            }
+        }
+    }
+}
+
+// db[i] (+)= sum over the splits' partial sums, in split order.
+template <typename O>
+__global__ __launch_bounds__(256) void gmm_reduce_kernel(const float* __restrict__ part, long long n, int splits,
+                                                         int accumulate, O* __restrict__ out)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    float v = 0.f;
+    for (int s = 0; s < splits; ++s) v += part[s * n + i];
+    if constexpr (std::is_same<O, float>::value) {
+        if (accumulate) v += out[i];
+        out[i] = v;
+    } else {
+        out[i] = from_f32<O>(v);
+    }
+}
+
+// ------------------------------------------------------------------ bias gradient
+// dbias[e][n] = sum of dc's rows of segment e.  Pass 1: one block per (row
+// range of an expert, 256 columns... see below) sums its rows in order in
+// fp32; pass 2 adds the ranges in order, so the result does not depend on
+// timing.
+constexpr int DB_COLS = 256;
+
+template <typename T>
+__global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, int splits, float* __restrict__ part)
+{
+    const int e = blockIdx.y, sp = blockIdx.z;
+    const int n = blockIdx.x * DB_COLS + threadIdx.x;
+    const Segment seg = segment_of(g.offsets, e, g.M);
+    const int len = seg.end - seg.begin, per = (len + splits - 1) / splits;
+    const int b = seg.begin + min(sp * per, len), t = seg.begin + min((sp + 1) * per, len);
+    if (n >= g.N) return;
+    const T* p = static_cast<const T*>(g.dc) + n;
+    float v = 0.f;
+    int s = b;
+    for (; s + 8 <= t; s += 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32(p[(size_t)(s + i) * g.ldc]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += x[i];
+    }
+    for (; s < t; ++s) v += to_f32(p[(size_t)s * g.ldc]);
+    part[((size_t)sp * g.E + e) * g.N + n] = v;
+}
+
+__global__ __launch_bounds__(256) void zero16_kernel(uint16_t* __restrict__ p, long long n)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
+template <typename T, typename O, int MODE, bool VEC, bool GATHER, typename Cfg>
+hipError_t launch_gathered(const GpArgs& g, hipStream_t s)
+{
+    long long grid;
+    if (MODE == GP_WGRAD) {
+        const long long nt = (g.K + Cfg::BR - 1) / Cfg::BR, mt = (g.N + Cfg::BC - 1) / Cfg::BC;
+        grid = (nt * mt + 7) / 8 * 8 * g.E * g.splits;
+    } else {
+        const long long nt = ((MODE == GP_FWD ? g.N : g.K) + Cfg::BR - 1) / Cfg::BR;
+        grid = (nt * ((g.M + Cfg::BC - 1) / Cfg::BC + g.E) + 7) / 8 * 8;
+    }
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((gmm_kernel<T, O, MODE, VEC, GATHER, Cfg>), dim3((unsigned)grid), dim3(Cfg::THREADS), 0, s, g);
+    return hipGetLastError();
+}
+
+template <typename T, typename O, int MODE, bool VEC, typename Cfg>
+hipError_t launch_cfg(const GpArgs& g, hipStream_t s)
+{
+    if (MODE == GP_WGRAD && g.pairs) return launch_gathered<T, O, MODE, VEC, MODE == GP_WGRAD, Cfg>(g, s);
+    return launch_gathered<T, O, MODE, VEC, false, Cfg>(g, s);
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+template <typename T, typename O, int MODE>
+hipError_t launch_mode(const GpArgs& g, bool vec, bool small, hipStream_t s)
+{
+    if (vec)
+        return small ? launch_cfg<T, O, MODE, true, TileSmall>(g, s) : launch_cfg<T, O, MODE, true, TileLarge>(g, s);
+    return launch_cfg<T, O, MODE, false, TileSmall>(g, s);
+}
+
+GpArgs gp_args(const GmmArgs& a)
+{
+    GpArgs g;
+    memset(&g, 0, sizeof g);
+    g.M = a.M;
+    g.N = a.N;
+    g.K = a.K;
+    g.E = a.E;
+    g.a_rows = a.a_rows;
+    g.k_shift = a.k > 1 ? 34 : 0;
+    g.k_magic = a.k > 1 ? ((1ull << 34) + a.k - 1) / a.k : 1;
+    g.lda = a.lda;
+    g.ldc = a.ldc;
+    g.offsets = a.offsets;
+    g.pairs = a.pairs;
+    g.a = a.a;
+    g.b = a.b;
+    g.bias = a.bias;
+    g.dc = a.dc;
+    g.out = a.out;
+    g.splits = 1;
+    return g;
+}
+
+template <int MODE>
+hipError_t launch_types(const GmmArgs& a, const GpArgs& g, bool vec, bool small, hipStream_t s)
+{
+    if (a.dtype == DT_BF16)
+        return a.out_dtype == DT_F32 ? launch_mode<bf16_t, float, MODE>(g, vec, small, s)
+                                     : launch_mode<bf16_t, bf16_t, MODE>(g, vec, small, s);
+    return a.out_dtype == DT_F32 ? launch_mode<f16_t, float, MODE>(g, vec, small, s)
+                                 : launch_mode<f16_t, f16_t, MODE>(g, vec, small, s);
+}
+
+// The 256 x 256 tile once an expert's share of the rows can fill most of it.
+bool use_small_tile(const GmmArgs& a) { return (long long)a.M < 128ll * a.E; }
+
+}  // namespace
+
+hipError_t launch_zero16(void* p, int64_t n, hipStream_t s)
+{
+    if (!p || n <= 0) return hipSuccess;
+    hipLaunchKernelGGL(zero16_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, static_cast<uint16_t*>(p),
+                       (long long)n);
+    return hipGetLastError();
+}
+
+hipError_t launch_gmm_forward(const GmmArgs& a, hipStream_t s)
+{
+    const GpArgs g = gp_args(a);
+    const bool vec = aligned16(a.a) && aligned16(a.b) && a.K % 8 == 0 && a.lda % 8 == 0;
+    return launch_types<GP_FWD>(a, g, vec, use_small_tile(a), s);
+}
+
+hipError_t launch_gmm_dgrad(const GmmArgs& a, hipStream_t s)
+{
+    const GpArgs g = gp_args(a);
+    const bool vec = aligned16(a.dc) && aligned16(a.b) && a.K % 8 == 0 && a.N % 8 == 0 && a.ldc % 8 == 0;
+    return launch_types<GP_DGRAD>(a, g, vec, use_small_tile(a), s);
+}
+
+int gmm_wgrad_splits(int M, int N, int K, int E)
+{
+    const long long tiles = (long long)((N + 255) / 256) * ((K + 255) / 256) * E;
+    if (tiles >= 256) return 1;
+    // at least 512 rows of an average expert per range: below that the extra
+    // pass over the partial sums costs more than the shorter loops give
+    const long long by_rows = (long long)M / E / 512, by_tiles = 256 / tiles;
+    const long long sp = by_rows < by_tiles ? by_rows : by_tiles;
+    return sp < 1 ? 1 : sp > 64 ? 64 : (int)sp;
+}
+
+int gmm_dbias_splits(int M, int E)
+{
+    const long long sp = (long long)M / E / 64;
+    return sp < 1 ? 1 : sp > 32 ? 32 : (int)sp;
+}
+
+hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
+{
+    GpArgs g = gp_args(a);
+    g.splits = a.splits;
+    g.accumulate = a.accumulate;
+    const bool vec = aligned16(a.a) && aligned16(a.dc) && a.K % 8 == 0 && a.N % 8 == 0 && a.lda % 8 == 0 &&
+                     a.ldc % 8 == 0;
+    const bool small = (long long)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E * a.splits < 256;
+    hipError_t err;
+    if (a.splits > 1) {
+        g.out = a.part;
+        g.accumulate = 0;
+        GmmArgs p = a;
+        p.out_dtype = DT_F32;
+        if ((err = launch_types<GP_WGRAD>(p, g, vec, small, s)) != hipSuccess) return err;
+        const long long n = (long long)a.E * a.N * a.K;
+        const dim3 grid((unsigned)((n + 255) / 256));
+        if (a.out_dtype == DT_F32)
+            hipLaunchKernelGGL(gmm_reduce_kernel<float>, grid, dim3(256), 0, s, a.part, n, a.splits, a.accumulate,
+                               static_cast<float*>(a.out));
+        else if (a.dtype == DT_BF16)
+            hipLaunchKernelGGL(gmm_reduce_kernel<bf16_t>, grid, dim3(256), 0, s, a.part, n, a.splits, 0,
+                               static_cast<bf16_t*>(a.out));
+        else
+            hipLaunchKernelGGL(gmm_reduce_kernel<f16_t>, grid, dim3(256), 0, s, a.part, n, a.splits, 0,
+                               static_cast<f16_t*>(a.out));
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    } else if ((err = launch_types<GP_WGRAD>(a, g, vec, small, s)) != hipSuccess) {
+        return err;
+    }
+    if (!a.dbias) return hipSuccess;
+    const int sp = gmm_dbias_splits(a.M, a.E);
+    const dim3 grid((a.N + DB_COLS - 1) / DB_COLS, a.E, sp);
+    if (a.dtype == DT_BF16)
+        hipLaunchKernelGGL(dbias_partial_kernel<bf16_t>, grid, dim3(DB_COLS), 0, s, g, sp, a.dbias_part);
+    else
+        hipLaunchKernelGGL(dbias_partial_kernel<f16_t>, grid, dim3(DB_COLS), 0, s, g, sp, a.dbias_part);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    const long long n = (long long)a.E * a.N;
+    hipLaunchKernelGGL(gmm_reduce_kernel<float>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.dbias_part, n,
+                       sp, a.accumulate, a.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace moe
