@@ -102,6 +102,20 @@ __device__ __forceinline__ void dma16(const void* src, const void* lds)
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
+// The same for 2 and 1 bytes of every lane, each landing zero-extended in the
+// 4-byte LDS word lds + 4 l.
+__device__ __forceinline__ void dma_u16(const void* src, const void* lds)
+{
+    typedef __attribute__((address_space(3))) const void* lds_t;
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" ::"s"(at), "v"(src) : "memory");
+}
+__device__ __forceinline__ void dma_u8(const void* src, const void* lds)
+{
+    typedef __attribute__((address_space(3))) const void* lds_t;
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(at), "v"(src) : "memory");
+}
 // Wait until at most N vector-memory operations of this wave are outstanding
 // (they complete in order).
 template <int N>

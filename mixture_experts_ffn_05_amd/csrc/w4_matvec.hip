@@ -1,0 +1,405 @@
+// Products of few rows with 4-bit weights (decoding).
+//
+//   v[s][n] = sum_i x[r(s)][i] scale[n][i / group] (code[n][i] - zero[n][i / group]) + bias[n]
+// and, for SwiGLU, y[s][n] = silu(v[s][n]) v[s][N/2 + n].  The codes are the
+// traffic; every one is read once per XR rows of an expert.
+//
+// An item is 32 weight rows (for SwiGLU 16 gate rows and the matching 16 up
+// rows) times up to XR rows of x.  A wave streams its items' K in chunks of 256
+// columns through its own ring of LDS slots, filled by direct-to-LDS loads
+// that run on into the next item: no barrier, no bubble between items, and
+// 4 KB of codes per slot always in flight.  A slot holds 128 bytes (whole
+// cache lines) of each weight row, the chunk's scales and zero points and the
+// x rows' same columns, so nothing but LDS is read in the loop.  With few items
+// (KS = 4) the 4 waves of a workgroup share an item, every fourth chunk each,
+// and add up through LDS.
+//
+// v_mfma_f32_16x16x32 takes x's rows as its A rows and weight rows as its B
+// columns, so a lane's four results are four rows of x for one n: a group's
+// scale and zero point are one value per lane.  Codes become 16-bit floats
+// without arithmetic: a code placed in the mantissa of 16.0 is exactly 16 +
+// code (a shift and an and-or for two codes).  Per group the matrix cores sum
+// D = sum (16 + code) x and, against a matrix of ones, S = sum x; then
+// v += scale (D - (16 + zero) S) in fp32.  Nothing is rounded between the code
+// and the fp32 sum.  The two codes of a word that share a register are 4 apart;
+// x's fragments are permuted to match (four byte permutes, shared by both
+// 16-row tiles).
+#include <string.h>
+
+#include <type_traits>
+
+#include "elem16.h"
+#include "moe_ops.h"
+#include "tile_sched.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int WQ_NW = 4;  // waves per workgroup
+constexpr int WQ_THREADS = WQ_NW * WAVE;
+constexpr int WQ_CK = 256;    // columns per chunk
+constexpr int WQ_DEPTH = 2;   // ring slots per wave
+constexpr int WQ_ROWB = WQ_CK / 2;
+
+__device__ uint32_t wq_zeros[4] __attribute__((aligned(16)));  // never written
+
+struct WqArgs {
+    int M, N, K, E, x_rows, k;
+    int group, swiglu, out_f32;
+    const int32_t* offsets;
+    const int32_t* pairs;
+    const void* x;
+    const uint8_t* codes;
+    const void* scales;
+    const uint8_t* zeros;
+    const void* bias;
+    void* out;
+};
+
+template <typename T>
+struct Code16;  // codes in the mantissa of 16.0
+template <>
+struct Code16<bf16_t> {
+    static constexpr uint32_t one = 0x3F803F80u;  // (1.0, 1.0)
+    static __device__ __forceinline__ u32x4 decode(uint32_t w)
+    {
+        constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
+        return u32x4{((w << 3) & m) | b, ((w >> 1) & m) | b, ((w >> 5) & m) | b, ((w >> 9) & m) | b};
+    }
+};
+template <>
+struct Code16<f16_t> {
+    static constexpr uint32_t one = 0x3C003C00u;
+    static __device__ __forceinline__ u32x4 decode(uint32_t w)
+    {
+        constexpr uint32_t m = 0x03C003C0u, b = 0x4C004C00u;
+        return u32x4{((w << 6) & m) | b, ((w << 2) & m) | b, ((w >> 2) & m) | b, ((w >> 6) & m) | b};
+    }
+};
+
+// Elements (0,1)(2,3)(4,5)(6,7) -> (0,4)(1,5)(2,6)(3,7).
+__device__ __forceinline__ u32x4 pair_by_four(u32x4 v)
+{
+    return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
+                 __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
+}
+
+typedef __attribute__((address_space(4))) const int32_t* wq_cptr;  // read through the scalar unit
+
+// GB: 32-column blocks per group.  Z: zero points given (else 8).  XR: rows of
+// x per item.  KS: waves that share an item's K.
+template <typename T, int GB, bool Z, int XR, int KS>
+__global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
+{
+    static_assert(KS == 1 || KS == WQ_NW, "an item belongs to a wave or to a workgroup");
+    constexpr int GPC = 8 / GB;                     // groups per chunk
+    constexpr int WBYTES = 32 * WQ_ROWB, XBYTES = XR * 2 * WQ_CK, SBYTES = 32 * GPC * 4;
+    constexpr int SLOT = WBYTES + XBYTES + (Z ? 2 : 1) * SBYTES;
+    constexpr int WL = WBYTES / 1024, XL = XBYTES / 1024, SL = 32 * GPC / WAVE;  // loads per slot
+    constexpr int NL = WL + XL + (Z ? 2 : 1) * SL;
+    static_assert(XL >= 1 && (WQ_DEPTH - 1) * NL < 64, "load count");
+    __shared__ __attribute__((aligned(16))) uint8_t sh[WQ_NW * WQ_DEPTH * SLOT];
+    __shared__ f32x4 red[KS > 1 ? 2 * WQ_NW * 2 * WAVE : 1];
+
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+    const int l16 = lane & 15, kg = lane >> 4;
+    const bool swiglu = g.swiglu;
+    const int half = g.N / 2, G = (g.K + g.group - 1) / g.group;
+    const int nchunks = (g.K + WQ_CK - 1) / WQ_CK;
+    const int tiles = swiglu ? (half + 15) / 16 : (g.N + 31) / 32;
+    uint8_t* ring = sh + wave * WQ_DEPTH * SLOT;
+    const int cw = KS > 1 ? wave : 0;  // first chunk of this wave
+
+    // ---- every expert's segment, one per lane (E <= 256), and its first item
+    int seg_b[4], seg_n[4], first[4], items = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        seg_b[j] = seg_n[j] = first[j] = 0;
+        if (WAVE * j >= g.E) continue;  // uniform
+        const int e = lane + WAVE * j;
+        if (e < g.E) {
+            const Segment sg = segment_of(g.offsets, e, g.M);
+            seg_b[j] = sg.begin;
+            seg_n[j] = sg.end - sg.begin;
+        }
+        const int n = (seg_n[j] + XR - 1) / XR * tiles;
+        const int excl = wave_excl_scan(n);
+        first[j] = items + excl;
+        items += __shfl(excl + n, WAVE - 1, WAVE);
+    }
+    items = __builtin_amdgcn_readfirstlane(items);
+    const int stride = KS > 1 ? (int)gridDim.x : (int)gridDim.x * WQ_NW;
+
+    struct Item {
+        int e, s0, s1, n0;  // expert, rows [s0, s1) of x (at most XR), first output column
+    };
+    auto locate = [&](int it) {
+        Item r{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (WAVE * j >= g.E) continue;
+            const int n = (seg_n[j] + XR - 1) / XR * tiles;
+            const uint64_t hit = ballot(n > 0 && it >= first[j] && it < first[j] + n);
+            if (hit) {
+                const int src = (int)__builtin_ctzll(hit);
+                const int local = it - __builtin_amdgcn_readlane(first[j], src);
+                const int pass = local / tiles;
+                r.e = WAVE * j + src;
+                r.s0 = __builtin_amdgcn_readlane(seg_b[j], src) + pass * XR;
+                r.s1 = min(r.s0 + XR, __builtin_amdgcn_readlane(seg_b[j], src) + __builtin_amdgcn_readlane(seg_n[j], src));
+                r.n0 = (local - pass * tiles) * (swiglu ? 16 : 32);
+            }
+        }
+        return r;
+    };
+    // Weight row of an item's row i (0..31), clamped to the matrix.
+    auto wrow = [&](const Item& t, int i) {
+        const int n = min(t.n0 + (i & 15), half - 1);
+        return swiglu ? (i < 16 ? n : half + n) : min(t.n0 + i, g.N - 1);
+    };
+
+    // ---- issue side: sources of the item being loaded.  Weights: load i
+    // covers 8 rows of 128 bytes, piece p of row r lying at p ^ (r / 2 % 8); x:
+    // 2 rows of 512 bytes, piece p of row r at p ^ (r % 16): the 16 rows that
+    // one fragment read touches fall on different banks.
+    const uintptr_t zeros = reinterpret_cast<uintptr_t>(wq_zeros);
+    uintptr_t wsrc[WL], xsrc[XL], ssrc[SL], zsrc[Z ? SL : 1];
+    int xlim[XL];
+    const int wk = 32 * ((lane & 7) ^ ((lane >> 4) & 3));  // + 32 * ((4 i) & 7): row 8 i + lane / 8
+    auto open = [&](const Item& t) {
+        const size_t erow = (size_t)t.e * g.N;
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+            const int r = 8 * i + (lane >> 3), p = (lane & 7) ^ ((r >> 1) & 7);
+            wsrc[i] = reinterpret_cast<uintptr_t>(g.codes) + (erow + wrow(t, r)) * (size_t)(g.K / 2) + 16 * p;
+        }
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            const int q = lane + WAVE * i;
+            const size_t at = (erow + wrow(t, q / GPC)) * G + q % GPC;
+            ssrc[i] = reinterpret_cast<uintptr_t>(g.scales) + 2 * at;
+            if (Z) zsrc[i] = reinterpret_cast<uintptr_t>(g.zeros) + at;
+        }
+        wq_cptr ids = (wq_cptr)(uintptr_t)g.pairs;
+#pragma unroll
+        for (int i = 0; i < XL; ++i) {
+            int row[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int s = t.s0 + 2 * i + h;
+                row[h] = s < t.s1 ? s : -1;
+                if (g.pairs) {  // uniform
+                    const int p = ids[min(s, t.s1 - 1)];
+                    row[h] = s < t.s1 && p >= 0 ? p / g.k : -1;
+                }
+                if (row[h] >= g.x_rows) row[h] = -1;
+            }
+            const int r = 2 * i + (lane >> 5), src = lane < 32 ? row[0] : row[1];
+            const int p = (lane & 31) ^ (r & 15);
+            xlim[i] = src >= 0 ? g.K - 8 * p : 0;
+            xsrc[i] = reinterpret_cast<uintptr_t>(g.x) + ((size_t)max(src, 0) * g.K + 8 * p) * 2;
+        }
+    };
+    // Chunk c of the open item into a slot; chunks at or past nchunks read zeros only.
+    auto issue = [&](int c, int slot) {
+        uint8_t* at = ring + slot * SLOT;
+        const int k0 = c * WQ_CK;
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+            const int k = wk ^ (i & 1 ? 128 : 0);  // rows 8 i + ..: r / 2 % 8 differs by 4 between odd and even i
+            dma16(reinterpret_cast<const void*>(k0 + k < g.K ? wsrc[i] + (size_t)c * WQ_ROWB : zeros), at + 1024 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < XL; ++i)
+            dma16(reinterpret_cast<const void*>(k0 < xlim[i] ? xsrc[i] + 2 * (size_t)k0 : zeros), at + WBYTES + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < SL; ++i) {
+            const bool ok = c * GPC + (lane + WAVE * i) % GPC < G;
+            dma_u16(reinterpret_cast<const void*>(ok ? ssrc[i] + 2 * (size_t)(c * GPC) : zeros),
+                    at + WBYTES + XBYTES + 256 * i);
+            if constexpr (Z)
+                dma_u8(reinterpret_cast<const void*>(ok ? zsrc[i] + (size_t)(c * GPC) : zeros),
+                       at + WBYTES + XBYTES + SBYTES + 256 * i);
+        }
+    };
+
+    int it = KS > 1 ? (int)blockIdx.x : (int)blockIdx.x * WQ_NW + wave;
+    if (it >= items) return;  // uniform per item owner
+    Item cur = locate(it), next_item = cur;
+    int iit = it, ic = cw;  // item and chunk to load next
+    open(cur);
+    auto advance = [&](int slot) {  // load the next chunk of this wave's stream
+        if (iit < items && ic >= nchunks) {
+            iit += stride;
+            ic = cw;
+            if (iit < items) {
+                next_item = locate(iit);
+                open(next_item);
+            }
+        }
+        issue(iit < items ? ic : nchunks, slot);
+        ic += KS;
+    };
+#pragma unroll
+    for (int d = 0; d < WQ_DEPTH; ++d) {
+        if (cw < nchunks) advance(d);
+    }
+
+    const u32x4 ones = u32x4{Code16<T>::one, Code16<T>::one, Code16<T>::one, Code16<T>::one};
+    int slot = 0, parity = 0;
+    for (; it < items; it += stride) {
+        cur = locate(it);
+        f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+        for (int c = cw; c < nchunks; c += KS) {
+            dma_wait<(WQ_DEPTH - 1) * NL>();
+            const uint8_t* at = ring + slot * SLOT;
+            const uint32_t* st = reinterpret_cast<const uint32_t*>(at + WBYTES + XBYTES);
+#pragma unroll
+            for (int q = 0; q < GPC; ++q) {
+                f32x4 dsum[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}, xsum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < GB; ++b) {
+                    const int j = q * GB + b, xr = l16 & (XR - 1);
+                    const u32x4 a = pair_by_four(
+                        *reinterpret_cast<const u32x4*>(at + WBYTES + xr * (2 * WQ_CK) + (((4 * j + kg) ^ xr) << 4)));
+                    xsum = mfma16_t(a, ones, xsum, T{});
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int r = 16 * n + l16;
+                        const uint32_t w =
+                            *reinterpret_cast<const uint32_t*>(at + r * WQ_ROWB + ((j ^ ((r >> 1) & 7)) << 4) + 4 * kg);
+                        dsum[n] = mfma16_t(a, Code16<T>::decode(w), dsum[n], T{});
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int r = 16 * n + l16;
+                    const float sc = to_f32(T{(uint16_t)st[r * GPC + q]});
+                    const float z = Z ? 16.f + (float)(st[32 * GPC + r * GPC + q] & 15u) : 24.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(sc, fmaf(-z, xsum[i], dsum[n][i]), acc[n][i]);
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this slot's reads are done
+            advance(slot);
+            slot = slot + 1 == WQ_DEPTH ? 0 : slot + 1;
+        }
+
+        // ---- the item's results
+        if constexpr (KS > 1) {  // two buffers by turns: one barrier an item
+            f32x4* buf = red + parity * (WQ_NW * 2 * WAVE);
+            parity ^= 1;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) buf[(wave * 2 + n) * WAVE + lane] = acc[n];
+            lds_barrier();
+            if (wave >= (swiglu ? 1 : 2)) continue;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (!swiglu && n != wave) continue;
+                acc[n] = buf[n * WAVE + lane];
+#pragma unroll
+                for (int w = 1; w < WQ_NW; ++w) acc[n] += buf[(w * 2 + n) * WAVE + lane];
+            }
+        }
+        const T* bias = g.bias ? static_cast<const T*>(g.bias) + (size_t)cur.e * g.N : nullptr;
+        const int cols = swiglu ? half : g.N;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (swiglu ? n > 0 : KS > 1 && n != wave) continue;
+            const int col = cur.n0 + 16 * n + l16;
+            if (col >= cols) continue;
+            f32x4 v = acc[n];
+            const float b = bias ? to_f32(bias[col]) : 0.f;
+            if (swiglu) {
+                const float bu = bias ? to_f32(bias[half + col]) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = silu(v[i] + b) * (acc[1][i] + bu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += b;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * kg + i;
+                if (r >= XR || cur.s0 + r >= cur.s1) continue;
+                const size_t at = (size_t)(cur.s0 + r) * cols + col;
+                if (g.out_f32)
+                    static_cast<float*>(g.out)[at] = v[i];
+                else
+                    static_cast<T*>(g.out)[at] = from_f32<T>(v[i]);
+            }
+        }
+    }
+    dma_wait<0>();  // loads past the last chunk
+}
+
+constexpr int WQ_CUS = 256;
+
+template <typename T, int GB, bool Z, int XR>
+hipError_t launch_xr(const WqArgs& g, hipStream_t s)
+{
+    const long long tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
+    const long long items = tiles * ((g.M + XR - 1) / XR + (g.E == 1 ? 0 : g.E < g.M ? g.E : g.M));  // at most
+    // A wave per item once there are items for every wave of the chip twice over.
+    if (items >= 2 * 8 * WQ_CUS) {
+        const long long blocks = (items + WQ_NW - 1) / WQ_NW, most = 2 * WQ_CUS;
+        hipLaunchKernelGGL((w4_matvec_kernel<T, GB, Z, XR, 1>), dim3((unsigned)(blocks < most ? blocks : most)),
+                           dim3(WQ_THREADS), 0, s, g);
+    } else {
+        hipLaunchKernelGGL((w4_matvec_kernel<T, GB, Z, XR, WQ_NW>), dim3((unsigned)items), dim3(WQ_THREADS), 0, s, g);
+    }
+    return hipGetLastError();
+}
+
+// Rows of x per item: twice an expert's average share (its share varies), so
+// that a second pass over an expert's codes is rare, in the smallest form that
+// holds them; a wider one costs LDS space, and with it loads in flight.
+template <typename T, int GB, bool Z>
+hipError_t launch_rows(const WqArgs& g, hipStream_t s)
+{
+    const int want = g.E == 1 ? g.M : 2 * ((g.M + g.E - 1) / g.E);
+    if (want <= 4) return launch_xr<T, GB, Z, 4>(g, s);
+    if (want <= 8) return launch_xr<T, GB, Z, 8>(g, s);
+    return launch_xr<T, GB, Z, 16>(g, s);
+}
+
+template <typename T, int GB>
+hipError_t launch_zeros(const WqArgs& g, hipStream_t s)
+{
+    return g.zeros ? launch_rows<T, GB, true>(g, s) : launch_rows<T, GB, false>(g, s);
+}
+
+template <typename T>
+hipError_t launch_group(const WqArgs& g, hipStream_t s)
+{
+    return g.group == 32 ? launch_zeros<T, 1>(g, s) : g.group == 64 ? launch_zeros<T, 2>(g, s) : launch_zeros<T, 4>(g, s);
+}
+
+}  // namespace
+
+hipError_t launch_w4_matvec(const W4Args& a, hipStream_t s)
+{
+    WqArgs g;
+    memset(&g, 0, sizeof g);
+    g.M = a.M;
+    g.N = a.N;
+    g.K = a.K;
+    g.E = a.E;
+    g.x_rows = a.x_rows;
+    g.k = a.k;
+    g.group = a.group;
+    g.offsets = a.offsets;
+    g.pairs = a.pairs;
+    g.x = a.x;
+    g.codes = a.codes;
+    g.scales = a.scales;
+    g.zeros = a.zeros;
+    g.bias = a.bias;
+    g.out = a.out;
+    g.swiglu = a.swiglu;
+    g.out_f32 = a.out_dtype == DT_F32;
+    return a.dtype == DT_BF16 ? launch_group<bf16_t>(g, s) : launch_group<f16_t>(g, s);
+}
+
+}  // namespace moe
