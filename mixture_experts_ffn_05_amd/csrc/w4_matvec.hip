@@ -15,15 +15,17 @@
 // and add up through LDS.
 //
 // v_mfma_f32_16x16x32 takes x's rows as its A rows and weight rows as its B
-// columns, so a lane's four results are four rows of x for one n: a group's
-// scale and zero point are one value per lane.  Codes become 16-bit floats
-// without arithmetic: a code placed in the mantissa of 16.0 is exactly 16 +
-// code (a shift and an and-or for two codes).  Per group the matrix cores sum
-// D = sum (16 + code) x and, against a matrix of ones, S = sum x; then
+// columns, so a lane's four results are rows of x for one n: a group's scale and
+// zero point are one value per lane.  Codes become 16-bit floats without
+// arithmetic: a code placed in the mantissa of 16.0 is exactly 16 + code (a
+// shift and an and-or for two codes).  Per group the matrix cores sum D = sum
+// (16 + code) x and, against a matrix of ones, S = sum x; then
 // v += scale (D - (16 + zero) S) in fp32.  Nothing is rounded between the code
 // and the fp32 sum.  The two codes of a word that share a register are 4 apart;
 // x's fragments are permuted to match (four byte permutes, shared by both
-// 16-row tiles).
+// 16-row tiles).  With 4 or 8 rows of x the 16 A rows hold 4 or 2 groups side
+// by side, so that one correction serves as many groups: the vector work per
+// code, not the matrix cores, is what competes with the memory here.
 #include <string.h>
 
 #include <type_traits>
@@ -57,24 +59,21 @@ struct WqArgs {
     void* out;
 };
 
+// Codes in the mantissa of 16.0: pairs (0,4)(1,5)(2,6)(3,7) of a word's eight.
+// mask and base stay in registers, so that masking and joining are one
+// instruction (two literals would not fit it).
 template <typename T>
-struct Code16;  // codes in the mantissa of 16.0
-template <>
-struct Code16<bf16_t> {
-    static constexpr uint32_t one = 0x3F803F80u;  // (1.0, 1.0)
-    static __device__ __forceinline__ u32x4 decode(uint32_t w)
+struct Code16 {
+    static constexpr bool B = std::is_same<T, bf16_t>::value;
+    static constexpr uint32_t one = B ? 0x3F803F80u : 0x3C003C00u;  // (1.0, 1.0)
+    uint32_t mask = B ? 0x00780078u : 0x03C003C0u, base = B ? 0x41804180u : 0x4C004C00u;
+    __device__ __forceinline__ Code16() { asm("" : "+v"(mask), "+s"(base)); }
+    __device__ __forceinline__ u32x4 decode(uint32_t w) const
     {
-        constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
-        return u32x4{((w << 3) & m) | b, ((w >> 1) & m) | b, ((w >> 5) & m) | b, ((w >> 9) & m) | b};
-    }
-};
-template <>
-struct Code16<f16_t> {
-    static constexpr uint32_t one = 0x3C003C00u;
-    static __device__ __forceinline__ u32x4 decode(uint32_t w)
-    {
-        constexpr uint32_t m = 0x03C003C0u, b = 0x4C004C00u;
-        return u32x4{((w << 6) & m) | b, ((w << 2) & m) | b, ((w >> 2) & m) | b, ((w >> 6) & m) | b};
+        return B ? u32x4{((w << 3) & mask) | base, ((w >> 1) & mask) | base, ((w >> 5) & mask) | base,
+                         ((w >> 9) & mask) | base}
+                 : u32x4{((w << 6) & mask) | base, ((w << 2) & mask) | base, ((w >> 2) & mask) | base,
+                         ((w >> 6) & mask) | base};
     }
 };
 
@@ -89,18 +88,28 @@ typedef __attribute__((address_space(4))) const int32_t* wq_cptr;  // read throu
 
 // GB: 32-column blocks per group.  Z: zero points given (else 8).  XR: rows of
 // x per item.  KS: waves that share an item's K.
+template <int GB, bool Z, int XR, int KS>
+struct WqShape {
+    static constexpr int GPC = 8 / GB;  // groups per chunk
+    static constexpr int WBYTES = 32 * WQ_ROWB, XBYTES = XR * 2 * WQ_CK, SBYTES = 32 * GPC * 4;
+    static constexpr int SLOT = WBYTES + XBYTES + (Z ? 2 : 1) * SBYTES;
+    static constexpr int RING = WQ_NW * WQ_DEPTH * SLOT, RED = KS > 1 ? 2 * WQ_NW * 2 * WAVE : 1;
+    // Two workgroups per CU where their LDS fits: asking for them also keeps
+    // the matrix cores' results in ordinary registers.
+    static constexpr int WAVES_PER_SIMD = RING + RED * 16 <= 80 * 1024 ? 2 : 1;
+};
+
 template <typename T, int GB, bool Z, int XR, int KS>
-__global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
+__global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD)) void w4_matvec_kernel(WqArgs g)
 {
+    using S = WqShape<GB, Z, XR, KS>;
     static_assert(KS == 1 || KS == WQ_NW, "an item belongs to a wave or to a workgroup");
-    constexpr int GPC = 8 / GB;                     // groups per chunk
-    constexpr int WBYTES = 32 * WQ_ROWB, XBYTES = XR * 2 * WQ_CK, SBYTES = 32 * GPC * 4;
-    constexpr int SLOT = WBYTES + XBYTES + (Z ? 2 : 1) * SBYTES;
+    constexpr int GPC = S::GPC, WBYTES = S::WBYTES, XBYTES = S::XBYTES, SBYTES = S::SBYTES, SLOT = S::SLOT;
     constexpr int WL = WBYTES / 1024, XL = XBYTES / 1024, SL = 32 * GPC / WAVE;  // loads per slot
     constexpr int NL = WL + XL + (Z ? 2 : 1) * SL;
     static_assert(XL >= 1 && (WQ_DEPTH - 1) * NL < 64, "load count");
-    __shared__ __attribute__((aligned(16))) uint8_t sh[WQ_NW * WQ_DEPTH * SLOT];
-    __shared__ f32x4 red[KS > 1 ? 2 * WQ_NW * 2 * WAVE : 1];
+    __shared__ __attribute__((aligned(16))) uint8_t sh[S::RING];
+    __shared__ f32x4 red[S::RED];
 
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
     const int l16 = lane & 15, kg = lane >> 4;
@@ -246,6 +255,17 @@ __global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
         if (cw < nchunks) advance(d);
     }
 
+    // The 16 A rows of the matrix cores are XR rows of x times SLOTS groups: A
+    // row XR u + r holds row r in the columns of the set's group u and zeros
+    // elsewhere, so D's rows XR u + r are group u's sums alone, and a lane
+    // scales the sums of its own group: one correction for SPC groups.
+    constexpr int SLOTS = 16 / XR, SPC = SLOTS < GPC ? SLOTS : GPC;
+    const int my_slot = l16 / XR, xr = l16 % XR;         // of the A row this lane supplies
+    const int d_slot = min(4 * kg / XR, SPC - 1);        // of the D rows it receives
+    const Code16<T> code;
+    uint32_t mask[SLOTS];
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) mask[u] = my_slot == u ? ~0u : 0u;
     const u32x4 ones = u32x4{Code16<T>::one, Code16<T>::one, Code16<T>::one, Code16<T>::one};
     int slot = 0, parity = 0;
     for (; it < items; it += stride) {
@@ -256,27 +276,31 @@ __global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
             const uint8_t* at = ring + slot * SLOT;
             const uint32_t* st = reinterpret_cast<const uint32_t*>(at + WBYTES + XBYTES);
 #pragma unroll
-            for (int q = 0; q < GPC; ++q) {
+            for (int q = 0; q < GPC; q += SPC) {  // a set of groups
                 f32x4 dsum[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}, xsum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int b = 0; b < GB; ++b) {
-                    const int j = q * GB + b, xr = l16 & (XR - 1);
-                    const u32x4 a = pair_by_four(
-                        *reinterpret_cast<const u32x4*>(at + WBYTES + xr * (2 * WQ_CK) + (((4 * j + kg) ^ xr) << 4)));
+                    const int jx = (q + min(my_slot, SPC - 1)) * GB + b;  // block of this lane's A row
+                    u32x4 a = pair_by_four(
+                        *reinterpret_cast<const u32x4*>(at + WBYTES + xr * (2 * WQ_CK) + (((4 * jx + kg) ^ xr) << 4)));
                     xsum = mfma16_t(a, ones, xsum, T{});
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int r = 16 * n + l16;
-                        const uint32_t w =
-                            *reinterpret_cast<const uint32_t*>(at + r * WQ_ROWB + ((j ^ ((r >> 1) & 7)) << 4) + 4 * kg);
-                        dsum[n] = mfma16_t(a, Code16<T>::decode(w), dsum[n], T{});
+                    for (int u = 0; u < SPC; ++u) {
+                        const u32x4 am = SLOTS == 1 ? a : a & mask[u];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const int r = 16 * n + l16, j = (q + u) * GB + b;
+                            const uint32_t w =
+                                *reinterpret_cast<const uint32_t*>(at + r * WQ_ROWB + ((j ^ ((r >> 1) & 7)) << 4) + 4 * kg);
+                            dsum[n] = mfma16_t(am, code.decode(w), dsum[n], T{});
+                        }
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int r = 16 * n + l16;
-                    const float sc = to_f32(T{(uint16_t)st[r * GPC + q]});
-                    const float z = Z ? 16.f + (float)(st[32 * GPC + r * GPC + q] & 15u) : 24.f;
+                    const int si = (16 * n + l16) * GPC + q + d_slot;
+                    const float sc = to_f32(T{(uint16_t)st[si]});
+                    const float z = Z ? 16.f + (float)(st[32 * GPC + si] & 15u) : 24.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(sc, fmaf(-z, xsum[i], dsum[n][i]), acc[n][i]);
                 }
@@ -286,7 +310,16 @@ __global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
             slot = slot + 1 == WQ_DEPTH ? 0 : slot + 1;
         }
 
-        // ---- the item's results
+        // ---- the item's results: rows 4 kg % XR + i, summed over the slots
+        // (A rows of slots past SPC hold a copy of the last one's x: not summed)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (4 * kg / XR >= SPC) acc[n][i] = 0.f;
+                if constexpr (XR <= 8) acc[n][i] += __shfl_xor(acc[n][i], 32, WAVE);
+                if constexpr (XR <= 4) acc[n][i] += __shfl_xor(acc[n][i], 16, WAVE);
+            }
         if constexpr (KS > 1) {  // two buffers by turns: one barrier an item
             f32x4* buf = red + parity * (WQ_NW * 2 * WAVE);
             parity ^= 1;
@@ -321,7 +354,7 @@ __global__ __launch_bounds__(WQ_THREADS) void w4_matvec_kernel(WqArgs g)
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = 4 * kg + i;
+                const int r = 4 * kg + i;  // the first slot's lanes store
                 if (r >= XR || cur.s0 + r >= cur.s1) continue;
                 const size_t at = (size_t)(cur.s0 + r) * cols + col;
                 if (g.out_f32)
