@@ -26,7 +26,7 @@ __device__ __forceinline__ T from_f32(float f);
 template <>
 __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f)
 {
-    return bf16_t{(uint16_t)f32_to_bf16(f)};
+    return bf16_t{__builtin_bit_cast(uint16_t, (__bf16)f)};
 }
 template <>
 __device__ __forceinline__ f16_t from_f32<f16_t>(float f)
@@ -54,6 +54,12 @@ template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     return (uint32_t)from_f32<T>(lo).v | ((uint32_t)from_f32<T>(hi).v << 16);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<bf16_t>(float lo, float hi)  // one v_cvt_pk_bf16_f32
+{
+    typedef __attribute__((ext_vector_type(2))) float f32x2;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
 // 16 bytes at any element-aligned address: gfx950 serves unaligned vector

@@ -2,6 +2,8 @@
 // registers, row sums, and the counter-based dropout.
 #pragma once
 
+#include <type_traits>
+
 #include "elem16.h"
 #include "moe_ops.h"
 
@@ -113,38 +115,78 @@ __device__ __forceinline__ void load_param8(const void* p, bool f32, int v, int 
     }
 }
 
+// v of the lane that DPP control CTRL names.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __uint_as_float(
+        (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_value(float v, int l)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
+}
+
+// Sums of N values over the 64 lanes in a fixed order, the same in every lane:
+// within rows of 16 lanes by DPP (no LDS traffic; the values side by side, so
+// that one's wait states are another's work), then the four rows' sums read as
+// scalars.
+template <int N>
+__device__ __forceinline__ void wave_totals(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += dpp<0xB1>(v[i]);  // quad_perm 1,0,3,2
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += dpp<0x4E>(v[i]);  // quad_perm 2,3,0,1
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += dpp<0x141>(v[i]);  // row_half_mirror
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += dpp<0x140>(v[i]);  // row_mirror
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = (lane_value(v[i], 0) + lane_value(v[i], 16)) + (lane_value(v[i], 32) + lane_value(v[i], 48));
+}
+
+// Sums of N values over the waves of a workgroup (NW <= 8; waves in order),
+// after wave_totals: the waves leave theirs in LDS, [value][8 waves], and each
+// group of 8 lanes adds one value's.
+template <int N>
+__device__ __forceinline__ void group_totals(float (&v)[N], int nw, float* lds)
+{
+    const int lane = lane_id(), wave = threadIdx.x / WAVE;
+    __syncthreads();  // the previous sums have been read
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) lds[8 * i + wave] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        const int at = 8 * i + lane;
+        float x = (lane & 7) < nw && at < 8 * N ? lds[at] : 0.f;
+        x += dpp<0xB1>(x);
+        x += dpp<0x4E>(x);
+        x += dpp<0x141>(x);
+#pragma unroll
+        for (int k = 0; k < 8 && i + k < N; ++k) v[i + k] = lane_value(x, 8 * k);
+    }
+}
+
 // Sums of N values over the TPR threads of a row (TPR 64: one wave; otherwise
-// the whole workgroup, through LDS, waves added in order).  Every thread gets
-// the sums.
+// the whole workgroup).  Every thread gets the sums.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* lds)
 {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if constexpr (TPR > WAVE) {
-        constexpr int NW = TPR / WAVE;
-        const int wave = threadIdx.x / WAVE;
-        __syncthreads();  // the previous sums have been read
-        if (lane_id() == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) lds[wave * N + i] = v[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = lds[i];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) v[i] += lds[w * N + i];
-        }
-    }
+    wave_totals(v);
+    if constexpr (TPR > WAVE) group_totals(v, TPR / WAVE, lds);
 }
 
 // Dropout's random bits: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
 // random numbers: as easy as 1, 2, 3", 2011) at counter (column / 8, row,
-// offset), key seed; 16 bits for each of the 8 columns, low halves first.  Bit
-// i of the result: column i is kept.
-__device__ __forceinline__ uint32_t dropout_keep8(uint32_t v, uint32_t row, uint64_t seed, uint64_t offset,
-                                                  uint32_t threshold)
+// offset), key seed; 16 bits for each of the 8 columns, low halves first.
+// keep[i]: column i is kept.
+__device__ __forceinline__ void dropout_keep8(uint32_t v, uint32_t row, uint64_t seed, uint64_t offset,
+                                              uint32_t threshold, bool (&keep)[8])
 {
     uint32_t c0 = v, c1 = row, c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
     uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
@@ -159,13 +201,8 @@ __device__ __forceinline__ uint32_t dropout_keep8(uint32_t v, uint32_t row, uint
         k1 += 0xBB67AE85u;
     }
     const uint32_t w[4] = {c0, c1, c2, c3};
-    uint32_t keep = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t bits = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
-        keep |= (bits >= threshold ? 1u : 0u) << i;
-    }
-    return keep;
+    for (int i = 0; i < 8; ++i) keep[i] = (i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu) >= threshold;
 }
 
 constexpr int NK_NONE = 0, NK_RMS = 1, NK_LAYER = 2;

@@ -21,7 +21,7 @@ namespace {
 template <typename T, int TPR, int NV, bool OUT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormArgs a)
 {
-    __shared__ float lds[2 * (TPR / WAVE)];
+    __shared__ float lds[TPR > WAVE ? 8 : 1];
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     const int t = blockIdx.x * RPB + (int)threadIdx.x / TPR;
     if (t >= a.T) return;  // uniform per wave; per block where a row spans waves
@@ -91,9 +91,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormArg
         }
         if constexpr (OUT) {
             if (a.drop_threshold) {  // a dropped element is 0, whatever it was
-                const uint32_t keep = dropout_keep8(v, t, seed, offset, a.drop_threshold);
+                bool keep[8];
+                dropout_keep8(v, t, seed, offset, a.drop_threshold, keep);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = keep >> j & 1u ? y[j] * a.drop_scale : 0.f;
+                for (int j = 0; j < 8; ++j) y[j] = keep[j] ? y[j] * a.drop_scale : 0.f;
             }
             if (gate_vec) {
 #pragma unroll
