@@ -108,6 +108,34 @@ __device__ __forceinline__ void dma16(const void* src, const void* lds)
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
 }
+// The same from base + offset (base uniform, offset a lane's bytes) to the LDS
+// address lds + AT (lds uniform, AT constant): no address arithmetic per load.
+__device__ __forceinline__ uintptr_t uniform_address(const void* p)
+{
+    const uint64_t v = (uint64_t)(uintptr_t)p;
+    return (uintptr_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32)) << 32);
+}
+template <int AT>
+__device__ __forceinline__ void dma16_at(const void* base, uint32_t offset, uint32_t lds)
+{
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3" ::"s"(lds), "n"(AT), "v"(offset),
+                 "s"(uniform_address(base))
+                 : "memory", "scc");
+}
+template <int AT>
+__device__ __forceinline__ void dma16_at(const void* src, uint32_t lds)
+{
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off" ::"s"(lds), "n"(AT), "v"(src)
+                 : "memory", "scc");
+}
+// LDS address of a shared object.
+__device__ __forceinline__ uint32_t lds_address(const void* p)
+{
+    typedef __attribute__((address_space(3))) const void* lds_t;
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_t)p);
+}
+
 // The same for 2 and 1 bytes of every lane, each landing zero-extended in the
 // 4-byte LDS word lds + 4 l.
 __device__ __forceinline__ void dma_u16(const void* src, const void* lds)

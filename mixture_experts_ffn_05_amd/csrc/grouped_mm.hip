@@ -55,6 +55,7 @@ struct TileCfg {
     static constexpr int BR = WR * WB * 32, BC = WC * TB * 32;
 };
 using TileLarge = TileCfg<2, 4, 4, 2>;  // 256 x 256, 8 waves
+using TileWide = TileCfg<2, 4, 5, 2>;   // 320 x 256, 8 waves
 using TileSmall = TileCfg<2, 2, 2, 1>;  // 128 x 64, 4 waves
 
 __device__ uint32_t gp_zeros[4] __attribute__((aligned(16)));  // never written
@@ -166,12 +167,11 @@ typedef __attribute__((address_space(4))) const int32_t* gp_cptr;  // read throu
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4* gp_trptr;
 
-// 8 elements from p on; those from element `left` on are 0.  p may be the
-// 16-byte block of zeros.
+// 8 elements from p on; those from element `left` on are 0.
 template <typename T>
-__device__ __forceinline__ u32x4 load8_masked(const T* p, const T* zeros, int left)
+__device__ __forceinline__ u32x4 load8_masked(const T* p, int left)
 {
-    if (left >= 8 || p == zeros) return load16_any(p);
+    if (left >= 8) return load16_any(p);
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -179,18 +179,25 @@ __device__ __forceinline__ u32x4 load8_masked(const T* p, const T* zeros, int le
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-// Order in which a half stage's NR LDS reads and NM MFMAs are issued: the
-// reads spread evenly among the MFMAs.
-template <int NR, int NM, int... I>
-__device__ __forceinline__ void gp_interleave(std::integer_sequence<int, I...>)
+// Order of a half stage: NQ LDS reads, then for every block row its NM MFMAs and
+// the NP reads that replace its operand.
+template <int NQ, int NM, int NP, int... I>
+__device__ __forceinline__ void gp_order(std::integer_sequence<int, I...>)
 {
+    __builtin_amdgcn_sched_group_barrier(0x100, NQ, 0);
     (
         [] {
-            constexpr int reads = NR * (I + 1) / NM - NR * I / NM;
-            if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            constexpr int reads = I >= 0 ? NP : 0;
+            __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
         }(),
         ...);
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void for_constants(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
 }
 
 // GATHER (wgrad): rows of a through pairs.  The forward gathers by `pairs`
@@ -200,9 +207,11 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
 {
     constexpr int BR = Cfg::BR, BC = Cfg::BC, NW = Cfg::NW, WB = Cfg::WB, TB = Cfg::TB;
     constexpr bool P_TR = MODE != GP_FWD, Q_TR = MODE == GP_WGRAD;
-    constexpr int DLP = BR * 64 / 1024 / NW, DLQ = BC * 64 / 1024 / NW;  // 1 KB loads per wave per stage
-    constexpr int L = DLP + DLQ;
-    static_assert(DLP >= 1 && DLQ >= 1, "a stage is whole loads");
+    // 1 KB loads per stage and wave; where the waves' shares of P differ, the
+    // last of them is the first waves' only.
+    constexpr int NLP = BR * 64 / 1024, DLP = (NLP + NW - 1) / NW, DLQ = BC * 64 / 1024 / NW;
+    constexpr int FULL = NLP - (DLP - 1) * NW;  // waves with DLP loads
+    static_assert(BR * 64 % 1024 == 0 && BC * 64 % (1024 * NW) == 0, "a stage is whole loads");
     __shared__ __attribute__((aligned(16))) uint8_t shp[GP_NBUF][BR * 64];
     __shared__ __attribute__((aligned(16))) uint8_t shq[GP_NBUF][BC * 64];
 
@@ -235,9 +244,12 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         if (e < 0) return;
     }
     int mt, ntile;
-    gm_band(local, mtiles, nt, &mt, &ntile);
+    e = __builtin_amdgcn_readfirstlane(e);
+    gm_band(__builtin_amdgcn_readfirstlane(local), __builtin_amdgcn_readfirstlane(mtiles), nt, &mt, &ntile);
     const int r0 = ntile * BR;
-    const Segment seg = segment_of(g.offsets, e, g.M);
+    Segment seg = segment_of(g.offsets, e, g.M);
+    seg.begin = __builtin_amdgcn_readfirstlane(seg.begin);
+    seg.end = __builtin_amdgcn_readfirstlane(seg.end);
     int J;       // contracted length
     int c0, c1;  // the tile's first column-role index and the end of its range
     int j0 = 0;  // WGRAD: first row of the split, relative to the segment
@@ -262,123 +274,179 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     const int wr = wave / Cfg::WC, wc = (wave + (Cfg::WC / 2) * wr) % Cfg::WC;
     const bool live = c0 + 32 * TB * wc < c1 && r0 + 32 * WB * wr < R;
 
-    // ---- sources of this wave's 1 KB loads.  Contiguous along j: load i covers
-    // tile rows 16 (wave + NW i) + lane / 4, lane l landing in 16-byte slot l %
-    // 4 of its row, which holds logical chunk (l % 4) ^ (row / 4 % 4).
+    // ---- sources of this wave's 1 KB loads: load i covers bytes 1024 (wave +
+    // NW i) .. of the tile, lane l its 16-byte piece l.  Contiguous along j: tile
+    // rows of 64 bytes; piece p of row r holds logical piece p ^ (r / 4 % 4).
     // Transposed: tile rows are j; a row of RB bytes holds its 64-byte segments
     // XORed with tr_xor(row), so that the four rows one transposing read
     // touches fall on different banks.
     const T* zeros = reinterpret_cast<const T*>(gp_zeros);
-    auto tr_xor = [](int row, int RB) { return RB >= 256 ? row & 3 : (row >> 1) & 1; };
     constexpr int PRB = BR * 2, QRB = BC * 2;
-    constexpr int PRPL = 1024 / PRB, QRPL = 1024 / QRB;  // rows per load of a transposed tile
+    auto tr_xor = [](int row, int RB) { return RB % 256 == 0 ? row & 3 : (row >> 1) & 1; };
+    const bool all_p = wave < FULL;
 
-    const T* psrc[DLP];  // row base (contiguous) or column base of row 0 (transposed)
-    const T* qsrc[DLQ];
-    int pj[DLP], qj[DLQ];  // contiguous: first j of the lane's chunk; transposed: its row
-    int plim[DLP], qlim[DLQ];  // end of the valid j; 0: no valid element at all
-    int pcol[DLP] = {}, qcol[DLQ] = {};  // transposed: first column
     const T* A = static_cast<const T*>(g.a);
     const T* B = static_cast<const T*>(g.b) + (size_t)e * g.N * g.K;
     const T* DC = static_cast<const T*>(g.dc);
-#pragma unroll
-    for (int i = 0; i < DLP; ++i) {
-        if constexpr (!P_TR) {
-            const int row = 16 * (wave + NW * i) + (lane >> 2);
-            pj[i] = 8 * ((lane & 3) ^ ((row >> 2) & 3));
-            const bool ok = r0 + row < R;
-            plim[i] = ok ? J : 0;
-            psrc[i] = ok ? B + (size_t)(r0 + row) * g.K : zeros;
-        } else {
-            const int row = PRPL * (wave + NW * i) + lane / (WAVE / PRPL), p = lane % (WAVE / PRPL);
-            pj[i] = row;
-            pcol[i] = r0 + 8 * ((((p >> 2) ^ tr_xor(row, PRB)) << 2) | (p & 3));
-            plim[i] = pcol[i] < R ? J : 0;
-            psrc[i] = (MODE == GP_DGRAD ? B : A) + (pcol[i] < R ? pcol[i] : 0);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < DLQ; ++i) {
-        if constexpr (!Q_TR) {
-            const int row = 16 * (wave + NW * i) + (lane >> 2);
-            const int s = c0 + row;
-            qj[i] = 8 * ((lane & 3) ^ ((row >> 2) & 3));
-            bool ok = s < c1;
-            int r = s;
-            if constexpr (MODE == GP_FWD) {
-                if (ok && g.pairs) r = input_row(g, g.pairs[s]);
-                ok = ok && (unsigned)r < (unsigned)g.a_rows;
-            }
-            qlim[i] = ok ? J : 0;
-            qsrc[i] = (MODE == GP_FWD ? A : DC) + (ok ? (size_t)r * (MODE == GP_FWD ? g.lda : g.ldc) : 0);
-        } else {
-            const int row = QRPL * (wave + NW * i) + lane / (WAVE / QRPL), p = lane % (WAVE / QRPL);
-            qj[i] = row;
-            qcol[i] = c0 + 8 * ((((p >> 2) ^ tr_xor(row, QRB)) << 2) | (p & 3));
-            qlim[i] = qcol[i] < c1 ? J : 0;
-            qsrc[i] = DC + (qcol[i] < c1 ? qcol[i] : 0);
-        }
-    }
+    // Load i of an operand: this lane's tile row, and its first column (contiguous
+    // along j: its first j).
+    auto p_row = [&](int i) { return !P_TR ? 16 * (wave + NW * i) + (lane >> 2) : (WAVE * (wave + NW * i) + lane) / (PRB / 16); };
+    auto q_row = [&](int i) { return !Q_TR ? 16 * (wave + NW * i) + (lane >> 2) : (WAVE * (wave + NW * i) + lane) / (QRB / 16); };
+    auto p_first = [&](int i) {
+        const int row = p_row(i), p = P_TR ? (WAVE * (wave + NW * i) + lane) % (PRB / 16) : lane & 3;
+        return 8 * (P_TR ? (((p >> 2) ^ tr_xor(row, PRB)) << 2) | (p & 3) : p ^ ((row >> 2) & 3));
+    };
+    auto q_first = [&](int i) {
+        const int row = q_row(i), p = Q_TR ? (WAVE * (wave + NW * i) + lane) % (QRB / 16) : lane & 3;
+        return 8 * (Q_TR ? (((p >> 2) ^ tr_xor(row, QRB)) << 2) | (p & 3) : p ^ ((row >> 2) & 3));
+    };
     // WGRAD with gathered rows: the pair ids of the next stage's rows, read
     // one stage early through the scalar unit (vector loads would have to be
     // waited for in order with the tiles in flight).
-    [[maybe_unused]] int prow[DLP][PRPL];
+    constexpr int PROWS = (1024 + PRB - 1) / PRB + (1024 % PRB != 0 ? 1 : 0);  // rows that one load may touch
+    [[maybe_unused]] int prow[DLP][PROWS];
     auto load_rows = [&](int st) {
         if constexpr (GATHER) {
             gp_cptr ids = (gp_cptr)(uintptr_t)g.pairs;
 #pragma unroll
             for (int i = 0; i < DLP; ++i) {
-                const int first = __builtin_amdgcn_readfirstlane(st * GP_BK + PRPL * (wave + NW * i));
+                const int first = st * GP_BK + 1024 * (wave + NW * i) / PRB;  // uniform
 #pragma unroll
-                for (int q = 0; q < PRPL; ++q) prow[i][q] = ids[seg.begin + j0 + min(first + q, J - 1)];
+                for (int q = 0; q < PROWS; ++q) prow[i][q] = ids[seg.begin + j0 + min(first + q, J - 1)];
             }
         }
-    };
-    // Source address of load i at stage st; the zeros past the operand's end.
-    // Branch-free: a branch here makes the compiler wait for every load in
-    // flight at the join.
-    auto pick = [&](bool ok, const T* src) {
-        return reinterpret_cast<const T*>(ok ? reinterpret_cast<uintptr_t>(src) : reinterpret_cast<uintptr_t>(zeros));
-    };
-    auto p_ok = [&](int i, int st) { return st * GP_BK + pj[i] < plim[i]; };
-    auto q_ok = [&](int i, int st) { return st * GP_BK + qj[i] < qlim[i]; };
-    auto p_at = [&](int i, int st) -> const T* {
-        const int j = st * GP_BK + pj[i];
-        if constexpr (!P_TR) {
-            return pick(p_ok(i, st), psrc[i] + j);
-        } else if constexpr (MODE == GP_DGRAD) {
-            return pick(p_ok(i, st), psrc[i] + (size_t)(unsigned)j * (unsigned)g.K);
-        } else {
-            int r = seg.begin + j0 + j;
-            if constexpr (GATHER) {
-                const int sub = lane / (WAVE / PRPL);
-                int p = prow[i][0];
-#pragma unroll
-                for (int q = 1; q < PRPL; ++q) p = sub == q ? prow[i][q] : p;
-                r = input_row(g, p);
-            }
-            return pick(p_ok(i, st) & ((unsigned)r < (unsigned)g.a_rows), psrc[i] + (long long)r * g.lda);
-        }
-    };
-    auto q_at = [&](int i, int st) -> const T* {
-        const int j = st * GP_BK + qj[i];
-        if constexpr (!Q_TR)
-            return pick(q_ok(i, st), qsrc[i] + j);
-        else
-            return pick(q_ok(i, st), qsrc[i] + (long long)(seg.begin + j0 + j) * g.ldc);
     };
 
-    // ---- VEC: direct-to-LDS loads of stage st
-    auto issue = [&](int st) {
-        const int buf = st % GP_NBUF;
+    // Source of load i at stage st with every bound checked: the zeros past the
+    // operand's end (or, for the register path, null).  Branch-free: a branch
+    // here makes the compiler wait for every load in flight at the join.
+    auto pick = [&](bool ok, const T* src) {
+        return reinterpret_cast<const T*>(ok ? reinterpret_cast<uintptr_t>(src)
+                                             : VEC ? reinterpret_cast<uintptr_t>(zeros) : (uintptr_t)0);
+    };
+    auto p_at = [&](int i, int st) -> const T* {
+        const int row = p_row(i), first = p_first(i);
+        if constexpr (!P_TR) {
+            const int j = st * GP_BK + first;
+            return pick((r0 + row < R) & (j < J), B + (long long)(r0 + row) * g.K + j);
+        } else {
+            const int j = st * GP_BK + row, col = r0 + first;
+            const bool ok = (col < R) & (j < J);
+            if constexpr (MODE == GP_DGRAD) return pick(ok, B + (long long)j * g.K + col);
+            int r = seg.begin + j0 + j;
+            if constexpr (GATHER) {
+                const int sub = row - 1024 * (wave + NW * i) / PRB;
+                int p = prow[i][0];
+#pragma unroll
+                for (int q = 1; q < PROWS; ++q) p = sub == q ? prow[i][q] : p;
+                r = input_row(g, p);
+            }
+            return pick(ok & ((unsigned)r < (unsigned)g.a_rows), A + (long long)r * g.lda + col);
+        }
+    };
+    // The input row of column-role index c of the forward product (-1: zeros).
+    auto fwd_row = [&](int c) {
+        if (!g.pairs) return c;
+        return c < c1 ? input_row(g, g.pairs[c]) : -1;
+    };
+    int qrow[MODE == GP_FWD ? DLQ : 1];  // forward: the rows of this wave's loads
+    if constexpr (MODE == GP_FWD) {
+#pragma unroll
+        for (int i = 0; i < DLQ; ++i) qrow[i] = c0 + q_row(i) < c1 ? fwd_row(c0 + q_row(i)) : -1;
+    }
+    auto q_at = [&](int i, int st) -> const T* {
+        const int row = q_row(i), first = q_first(i);
+        if constexpr (MODE == GP_FWD) {
+            const int j = st * GP_BK + first, r = qrow[i];
+            return pick((r >= 0) & (j < J), A + (long long)r * g.lda + j);
+        } else if constexpr (MODE == GP_DGRAD) {
+            const int j = st * GP_BK + first;
+            return pick((c0 + row < c1) & (j < J), DC + (long long)(c0 + row) * g.ldc + j);
+        } else {
+            const int j = st * GP_BK + row, col = c0 + first;
+            return pick((col < c1) & (j < J), DC + (long long)(seg.begin + j0 + j) * g.ldc + col);
+        }
+    };
+
+    // ---- VEC: direct-to-LDS loads.  Whole stages (32 valid j) use a uniform
+    // base that moves with the stage and fixed 32-bit offsets, so a load costs no
+    // vector arithmetic; rows and columns past the matrix's or the segment's end
+    // read a valid one instead (their results are not stored).  Gathered rows
+    // keep 64-bit addresses.  The last, partial stage checks every bound.
+    constexpr bool Q64 = MODE == GP_FWD;  // q rows anywhere in `a`
+    [[maybe_unused]] uint32_t poff[DLP], qoff[DLQ];
+    [[maybe_unused]] const T* qptr[DLQ];
+    const int nwhole = J / GP_BK;
+    const T* pbase = nullptr;
+    const T* qbase = nullptr;
+    long long pstep = GP_BK, qstep = GP_BK;  // elements per stage
+    if constexpr (VEC) {
+        if constexpr (MODE == GP_FWD) {
+            pbase = B + (size_t)r0 * g.K;
+        } else if constexpr (MODE == GP_DGRAD) {
+            pbase = B + r0;
+            pstep = (long long)GP_BK * g.K;
+            qbase = DC + (size_t)c0 * g.ldc;
+        } else {
+            pbase = A + (size_t)(seg.begin + j0) * g.lda + r0;
+            pstep = GP_BK * g.lda;
+            qbase = DC + (size_t)(seg.begin + j0) * g.ldc + c0;
+            qstep = GP_BK * g.ldc;
+        }
 #pragma unroll
         for (int i = 0; i < DLP; ++i) {
-            dma16(p_at(i, st), shp[buf] + 1024 * (wave + NW * i));
+            const int row = p_row(i), first = p_first(i);
+            if constexpr (!P_TR)
+                poff[i] = 2u * ((uint32_t)min(row, R - 1 - r0) * (uint32_t)g.K + first);
+            else
+                poff[i] = 2u * ((uint32_t)row * (uint32_t)(MODE == GP_DGRAD ? g.K : g.lda) + (r0 + first < R ? first : 0));
         }
 #pragma unroll
         for (int i = 0; i < DLQ; ++i) {
-            dma16(q_at(i, st), shq[buf] + 1024 * (wave + NW * i));
+            const int row = q_row(i), first = q_first(i);
+            if constexpr (Q64)
+                qptr[i] = A + (size_t)max(qrow[i], 0) * g.lda + first;
+            else if constexpr (!Q_TR)
+                qoff[i] = 2u * ((uint32_t)min(row, c1 - 1 - c0) * (uint32_t)g.ldc + first);
+            else
+                qoff[i] = 2u * ((uint32_t)row * (uint32_t)g.ldc + (c0 + first < c1 ? first : 0));
         }
+    }
+    const uint32_t lds_p = lds_address(shp[0]) + 1024 * wave, lds_q = lds_address(shq[0]) + 1024 * wave;
+    // A whole stage st into buffer BUF.
+    auto issue = [&](auto buf_c, int st) {
+        constexpr int BUF = decltype(buf_c)::value;
+        const T* pb = pbase + st * pstep;
+        const T* qb = qbase + st * qstep;
+        for_constants(
+            [&](auto i_c) {
+                constexpr int i = decltype(i_c)::value, at = BUF * BR * 64 + 1024 * NW * i;
+                if (FULL < NW && i == DLP - 1 && !all_p) return;  // uniform
+                if constexpr (GATHER)
+                    dma16_at<at>(p_at(i, st), lds_p);
+                else
+                    dma16_at<at>(pb, poff[i], lds_p);
+            },
+            std::make_integer_sequence<int, DLP>{});
+        for_constants(
+            [&](auto i_c) {
+                constexpr int i = decltype(i_c)::value, at = BUF * BC * 64 + 1024 * NW * i;
+                if constexpr (Q64)
+                    dma16_at<at>(qptr[i] + st * GP_BK, lds_q);
+                else
+                    dma16_at<at>(qb, qoff[i], lds_q);
+            },
+            std::make_integer_sequence<int, DLQ>{});
+        load_rows(st + 1);
+    };
+    // Any stage, bounds checked; past the last one zeros.
+    auto issue_any = [&](int st) {
+        const int buf = st % GP_NBUF;
+#pragma unroll
+        for (int i = 0; i < DLP; ++i)
+            if (FULL == NW || i < DLP - 1 || all_p) dma16_at<0>(p_at(i, st), lds_p + buf * BR * 64 + 1024 * NW * i);
+#pragma unroll
+        for (int i = 0; i < DLQ; ++i) dma16_at<0>(q_at(i, st), lds_q + buf * BC * 64 + 1024 * NW * i);
         load_rows(st + 1);
     };
     // ---- otherwise: through registers
@@ -387,21 +455,21 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         const u32x4 z = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < DLP; ++i) {
-            const int left = P_TR ? R - pcol[i] : J - (st * GP_BK + pj[i]);
-            rp[set][i] = p_ok(i, st) ? load8_masked(p_at(i, st), zeros, left) : z;
+            const T* src = p_at(i, st);
+            rp[set][i] = src ? load8_masked(src, P_TR ? R - (r0 + p_first(i)) : J - (st * GP_BK + p_first(i))) : z;
         }
 #pragma unroll
         for (int i = 0; i < DLQ; ++i) {
-            const int left = Q_TR ? c1 - qcol[i] : J - (st * GP_BK + qj[i]);
-            rq[set][i] = q_ok(i, st) ? load8_masked(q_at(i, st), zeros, left) : z;
+            const T* src = q_at(i, st);
+            rq[set][i] = src ? load8_masked(src, Q_TR ? c1 - (c0 + q_first(i)) : J - (st * GP_BK + q_first(i))) : z;
         }
         load_rows(st + 1);
     };
-    auto store = [&](int set, int st) {
-        const int buf = st % GP_NBUF;
+    auto store = [&](int set, int buf) {
 #pragma unroll
         for (int i = 0; i < DLP; ++i)
-            *reinterpret_cast<u32x4*>(shp[buf] + 1024 * (wave + NW * i) + 16 * lane) = rp[set][i];
+            if (FULL == NW || i < DLP - 1 || all_p)
+                *reinterpret_cast<u32x4*>(shp[buf] + 1024 * (wave + NW * i) + 16 * lane) = rp[set][i];
 #pragma unroll
         for (int i = 0; i < DLQ; ++i)
             *reinterpret_cast<u32x4*>(shq[buf] + 1024 * (wave + NW * i) + 16 * lane) = rq[set][i];
@@ -414,9 +482,6 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         for (int t = 0; t < TB; ++t) acc[m][t] = f32x16_t{};
 
     // ---- operand fragments of one 16-wide j step
-    struct Frags {
-        u32x4 p[WB], q[TB];
-    };
     const int r32 = lane & 31, kg = lane >> 5;
     // Transposing read: lane l addresses row l % 16 / 4 (+ 8 for the upper half
     // wave) and columns 16 (l / 16 % 2) + 4 (l % 4) .. +3 of a 32-column block,
@@ -435,37 +500,45 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         const int c = (2 * s + kg) ^ ((row >> 2) & 3);
         return *reinterpret_cast<const u32x4*>(tile + row * 64 + c * 16);
     };
-    auto load_frags = [&](int buf, int s, Frags& f) {
+    u32x4 p[WB], q[2][TB];
+    auto load_p = [&](int buf, int s, int m) {
+        if constexpr (P_TR)
+            p[m] = read_tr(shp[buf], PRB, WB * wr + m, s);
+        else
+            p[m] = read_row(shp[buf], 32 * (WB * wr + m) + r32, s);
+    };
+    auto load_q = [&](int buf, int s) {
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
             if constexpr (Q_TR)
-                f.q[t] = read_tr(shq[buf], QRB, TB * wc + t, s);
+                q[s][t] = read_tr(shq[buf], QRB, TB * wc + t, s);
             else
-                f.q[t] = read_row(shq[buf], 32 * (TB * wc + t) + r32, s);
+                q[s][t] = read_row(shq[buf], 32 * (TB * wc + t) + r32, s);
         }
+    };
+    // The MFMAs of step s, with the fragments of the next step (1 - s of buffer
+    // `next`) read among them: q into its other set first, p[m] in place once
+    // its own MFMAs are issued.
+    auto step = [&](auto s_c, int next) {
+        constexpr int S = decltype(s_c)::value;
+        load_q(next, 1 - S);
 #pragma unroll
         for (int m = 0; m < WB; ++m) {
-            if constexpr (P_TR)
-                f.p[m] = read_tr(shp[buf], PRB, WB * wr + m, s);
-            else
-                f.p[m] = read_row(shp[buf], 32 * (WB * wr + m) + r32, s);
+#pragma unroll
+            for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(p[m], q[S][t], acc[m][t], T{});
+            load_p(next, 1 - S, m);
         }
+        gp_order<TB*(Q_TR ? 2 : 1), TB, P_TR ? 2 : 1>(std::make_integer_sequence<int, WB>{});
     };
-    auto mma = [&](const Frags& f) {
-#pragma unroll
-        for (int m = 0; m < WB; ++m)
-#pragma unroll
-            for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(f.p[m], f.q[t], acc[m][t], T{});
-    };
-    constexpr int NR = WB * (P_TR ? 2 : 1) + TB * (Q_TR ? 2 : 1), NM = WB * TB;
-    auto interleave = [&]() { gp_interleave<NR, NM>(std::make_integer_sequence<int, NM>{}); };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
 
     // ---- software pipeline: each stage is two 16-wide steps; the barrier that
     // publishes stage st+1 sits between them.
     if (nstages > 0) {
         load_rows(0);
         if constexpr (VEC) {
-            for (int st = 0; st < 3; ++st) issue(st);
+            for (int st = 0; st < 3; ++st) issue_any(st);
             dma_wait<0>();
         } else {
             fetch(0, 0);
@@ -476,48 +549,62 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             fetch(1, 3);
         }
         lds_barrier();
-        Frags f0, f1;
-        if (live) load_frags(0, 0, f0);
-        auto stage = [&](int st, auto set_c) {  // set_c = st & 1, a constant so that the sets stay in registers
-            constexpr int SET = decltype(set_c)::value;
-            const int buf = st % GP_NBUF, nb = (st + 1) % GP_NBUF;
+        if (live) {
+            load_q(0, 0);
+#pragma unroll
+            for (int m = 0; m < WB; ++m) load_p(0, 0, m);
+        }
+        // Stage st in buffer buf; `load` starts the loads that follow the barrier.
+        auto stage = [&](int buf, int next, auto load) {
             __builtin_amdgcn_sched_barrier(0);
-            if (live) {
-                load_frags(buf, 1, f1);
-                mma(f0);
-                interleave();
-            }
+            if (live) step(S0{}, buf);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (VEC) dma_wait<L>();  // stage st+1 has landed; st+2's loads may be in flight
-            lds_barrier();                    // stage st+1 visible; the buffer of stage st-1 is free
-            if constexpr (VEC) {
-                issue(st + 3);
-            } else {
-                store(SET, st + 2);
-                fetch(SET, st + 4);
+            if constexpr (VEC) {  // stage st+1 has landed; st+2's loads may be in flight
+                if (FULL == NW || all_p)
+                    dma_wait<DLP + DLQ>();
+                else
+                    dma_wait<DLP + DLQ - 1>();
             }
+            lds_barrier();  // stage st+1 visible; the buffer of stage st-1 is free
+            load();
             __builtin_amdgcn_sched_barrier(0);
-            if (live) {
-                load_frags(nb, 0, f0);
-                mma(f1);
-                interleave();
-            }
+            if (live) step(S1{}, next);
         };
         int st = 0;
-        for (; st + 2 < nstages; st += 2) {
-            stage(st, std::integral_constant<int, 0>{});
-            stage(st + 1, std::integral_constant<int, 1>{});
-        }
-        if (st + 1 < nstages) {
-            stage(st, std::integral_constant<int, 0>{});
-            ++st;
+        if constexpr (VEC) {  // while the stages to load are whole: four at a time, buffers constant
+            for (; st + 6 < nwhole; st += 4)
+                for_constants(
+                    [&](auto b_c) {
+                        constexpr int BUF = decltype(b_c)::value;
+                        stage(BUF, (BUF + 1) % GP_NBUF,
+                              [&] { issue(std::integral_constant<int, (BUF + 3) % GP_NBUF>{}, st + BUF + 3); });
+                    },
+                    std::make_integer_sequence<int, 4>{});
+            for (; st + 1 < nstages; ++st) stage(st % GP_NBUF, (st + 1) % GP_NBUF, [&] { issue_any(st + 3); });
+        } else {
+            auto pair = [&](int s, auto set_c) {  // set_c = s & 1, a constant so that the sets stay in registers
+                constexpr int SET = decltype(set_c)::value;
+                stage(s % GP_NBUF, (s + 1) % GP_NBUF, [&] {
+                    store(SET, (s + 2) % GP_NBUF);
+                    fetch(SET, s + 4);
+                });
+            };
+            for (; st + 2 < nstages; st += 2) {
+                pair(st, S0{});
+                pair(st + 1, S1{});
+            }
+            if (st + 1 < nstages) {
+                pair(st, S0{});
+                ++st;
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
         if (live) {
-            load_frags(st % GP_NBUF, 1, f1);
-            mma(f0);
-            interleave();
-            mma(f1);
+            step(S0{}, st % GP_NBUF);
+#pragma unroll
+            for (int m = 0; m < WB; ++m)
+#pragma unroll
+                for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(p[m], q[1][t], acc[m][t], T{});
         }
         mfma_drain();
         dma_wait<0>();  // the surplus loads past the last stage
@@ -534,6 +621,14 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     } else {
         out = static_cast<O*>(g.out);
         ldo = MODE == GP_FWD ? g.ldc : g.lda;
+    }
+    bool zero_row[TB] = {};  // forward: a pair that names no input row
+    if constexpr (MODE == GP_FWD) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const int c = c0 + 32 * (TB * wc + t) + r32;
+            zero_row[t] = c < c1 && fwd_row(c) < 0;
+        }
     }
     const T* bias = MODE == GP_FWD && g.bias ? static_cast<const T*>(g.bias) + (size_t)e * g.N : nullptr;
 #pragma unroll
@@ -556,7 +651,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
                 O* at = out + (size_t)c * ldo + row;
                 float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = acc[m][t][4 * q + i] + bv[i];
+                for (int i = 0; i < 4; ++i) v[i] = (zero_row[t] ? 0.f : acc[m][t][4 * q + i]) + bv[i];
                 if constexpr (std::is_same<O, float>::value) {
                     if (MODE == GP_WGRAD && g.accumulate) {
 #pragma unroll
@@ -598,33 +693,49 @@ __global__ __launch_bounds__(256) void gmm_reduce_kernel(const float* __restrict
 }
 
 // ------------------------------------------------------------------ bias gradient
-// dbias[e][n] = sum of dc's rows of segment e.  Pass 1: one block per (row
-// range of an expert, 256 columns... see below) sums its rows in order in
-// fp32; pass 2 adds the ranges in order, so the result does not depend on
-// timing.
-constexpr int DB_COLS = 256;
+// dbias[e][n] = sum of dc's rows of segment e.  Pass 1: one workgroup per (row
+// range of an expert, 256 columns): 8 groups of 32 threads take every eighth row
+// of the range, 8 columns (16 bytes) a thread, in fp32, and are added in order;
+// pass 2 adds the ranges in order, so the result does not depend on timing.
+constexpr int DB_COLS = 256, DB_GROUPS = 8;
 
 template <typename T>
 __global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, int splits, float* __restrict__ part)
 {
-    const int e = blockIdx.y, sp = blockIdx.z;
-    const int n = blockIdx.x * DB_COLS + threadIdx.x;
+    __shared__ float sh[DB_GROUPS][DB_COLS];
+    const int e = blockIdx.y, sp = blockIdx.z, cv = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int n = blockIdx.x * DB_COLS + 8 * cv;
     const Segment seg = segment_of(g.offsets, e, g.M);
     const int len = seg.end - seg.begin, per = (len + splits - 1) / splits;
     const int b = seg.begin + min(sp * per, len), t = seg.begin + min((sp + 1) * per, len);
-    if (n >= g.N) return;
-    const T* p = static_cast<const T*>(g.dc) + n;
-    float v = 0.f;
-    int s = b;
-    for (; s + 8 <= t; s += 8) {
-        float x[8];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (n < g.N) {
+        const T* p = static_cast<const T*>(g.dc) + n;
+        auto row = [&](int s) {
+            return s < t ? load8_masked(p + (size_t)s * g.ldc, g.N - n) : u32x4{0, 0, 0, 0};
+        };
+        for (int s = b + grp; s < t; s += 4 * DB_GROUPS) {
+            u32x4 x[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32(p[(size_t)(s + i) * g.ldc]);
+            for (int i = 0; i < 4; ++i) x[i] = row(s + DB_GROUPS * i);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += x[i];
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[2 * j] += lo_f32<T>(x[i][j]);
+                    v[2 * j + 1] += hi_f32<T>(x[i][j]);
+                }
+        }
     }
-    for (; s < t; ++s) v += to_f32(p[(size_t)s * g.ldc]);
-    part[((size_t)sp * g.E + e) * g.N + n] = v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sh[grp][8 * cv + j] = v[j];
+    __syncthreads();
+    const int c = blockIdx.x * DB_COLS + threadIdx.x;
+    if (c >= g.N) return;
+    float s = sh[0][threadIdx.x];
+#pragma unroll
+    for (int q = 1; q < DB_GROUPS; ++q) s += sh[q][threadIdx.x];
+    part[((size_t)sp * g.E + e) * g.N + c] = s;
 }
 
 __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* __restrict__ p, long long n)
@@ -656,13 +767,37 @@ hipError_t launch_cfg(const GpArgs& g, hipStream_t s)
     return launch_gathered<T, O, MODE, VEC, false, Cfg>(g, s);
 }
 
+// Rows that the direct loads take: 16-byte aligned, and short enough that a
+// tile's offsets (at most 320 rows) fit 32 bits.
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool vec_stride(long long ld) { return ld % 8 == 0 && ld <= 4ll << 20; }
+
+// 320 or 256 tile rows: the one that covers the output's rows in less time.  A
+// workgroup fills a CU, so forward and dgrad run in rounds of 256 tiles (half a
+// tile more per expert for its ragged end), a round taking time in proportion
+// to the tile's rows; the weight gradient's tiles differ in length and go out
+// longest first, so there it is the rows covered that count.
+template <int MODE>
+bool wide_tile(const GpArgs& g)
+{
+    const int R = MODE == GP_FWD ? g.N : g.K;
+    auto cost = [&](int BR) {
+        const long long nt = (R + BR - 1) / BR;
+        if (MODE == GP_WGRAD) return nt * BR;
+        const long long tiles = nt * ((g.M + 255) / 256 + g.E / 2);
+        return (tiles + 255) / 256 * BR;
+    };
+    return cost(TileWide::BR) <= cost(TileLarge::BR);
+}
 
 template <typename T, typename O, int MODE>
 hipError_t launch_mode(const GpArgs& g, bool vec, bool small, hipStream_t s)
 {
-    if (vec)
-        return small ? launch_cfg<T, O, MODE, true, TileSmall>(g, s) : launch_cfg<T, O, MODE, true, TileLarge>(g, s);
+    if (vec) {
+        if (small) return launch_cfg<T, O, MODE, true, TileSmall>(g, s);
+        return wide_tile<MODE>(g) ? launch_cfg<T, O, MODE, true, TileWide>(g, s)
+                                  : launch_cfg<T, O, MODE, true, TileLarge>(g, s);
+    }
     return launch_cfg<T, O, MODE, false, TileSmall>(g, s);
 }
 
@@ -716,14 +851,14 @@ hipError_t launch_zero16(void* p, int64_t n, hipStream_t s)
 hipError_t launch_gmm_forward(const GmmArgs& a, hipStream_t s)
 {
     const GpArgs g = gp_args(a);
-    const bool vec = aligned16(a.a) && aligned16(a.b) && a.K % 8 == 0 && a.lda % 8 == 0;
+    const bool vec = aligned16(a.a) && aligned16(a.b) && a.K % 8 == 0 && vec_stride(a.lda);
     return launch_types<GP_FWD>(a, g, vec, use_small_tile(a), s);
 }
 
 hipError_t launch_gmm_dgrad(const GmmArgs& a, hipStream_t s)
 {
     const GpArgs g = gp_args(a);
-    const bool vec = aligned16(a.dc) && aligned16(a.b) && a.K % 8 == 0 && a.N % 8 == 0 && a.ldc % 8 == 0;
+    const bool vec = aligned16(a.dc) && aligned16(a.b) && a.K % 8 == 0 && a.N % 8 == 0 && vec_stride(a.ldc);
     return launch_types<GP_DGRAD>(a, g, vec, use_small_tile(a), s);
 }
 
@@ -749,8 +884,8 @@ hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
     GpArgs g = gp_args(a);
     g.splits = a.splits;
     g.accumulate = a.accumulate;
-    const bool vec = aligned16(a.a) && aligned16(a.dc) && a.K % 8 == 0 && a.N % 8 == 0 && a.lda % 8 == 0 &&
-                     a.ldc % 8 == 0;
+    const bool vec = aligned16(a.a) && aligned16(a.dc) && a.K % 8 == 0 && a.N % 8 == 0 && vec_stride(a.lda) &&
+                     vec_stride(a.ldc);
     const bool small = (long long)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E * a.splits < 256;
     hipError_t err;
     if (a.splits > 1) {
