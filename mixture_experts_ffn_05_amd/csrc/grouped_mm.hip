@@ -84,6 +84,9 @@ __device__ __forceinline__ int input_row(const GpArgs& g, int p)
     return ((p >= 0) & (r < g.a_rows)) ? r : -1;
 }
 
+// The schedule puts each expert's ragged last tile after its full ones: dealt
+// out at the very end instead, so that the last round is of short tiles, they lose
+// the L2's copies of their expert's rows (prefill product 1188 -> 1258 us).
 // M-tile `tile` of the schedule in which expert e owns ceil(len_e / BC) * nt
 // consecutive tiles; every wave computes the same.  Also returns the number of
 // tiles of all experts.
@@ -693,33 +696,63 @@ __global__ __launch_bounds__(256) void gmm_reduce_kernel(const float* __restrict
 }
 
 // ------------------------------------------------------------------ bias gradient
-// dbias[e][n] = sum of dc's rows of segment e.  Pass 1: one workgroup per (row
-// range of an expert, 256 columns): 8 groups of 32 threads take every eighth row
-// of the range, 8 columns (16 bytes) a thread, in fp32, and are added in order;
-// pass 2 adds the ranges in order, so the result does not depend on timing.
-constexpr int DB_COLS = 256, DB_GROUPS = 8;
+// dbias[e][n] = sum of dc's rows of segment e.  Pass 1: one workgroup per (range
+// of DB_ROWS rows of an expert, 256 columns): 8 groups of 32 threads take every
+// eighth row of the range, 8 columns (16 bytes) a thread, in fp32, and are added
+// in order; pass 2 adds an expert's ranges in order, so the result does not
+// depend on timing.
+constexpr int DB_COLS = 256, DB_GROUPS = 8, DB_ROWS = 128;
+
+// Ranges of the experts before e, and of e itself.
+__device__ __forceinline__ int dbias_ranges(const GpArgs& g, int e, int* own)
+{
+    int before = 0;
+    for (int base = 0; base <= e; base += WAVE) {
+        const int j = base + lane_id();
+        const Segment sg = j < g.E ? segment_of(g.offsets, j, g.M) : Segment{0, 0};
+        const int n = (sg.end - sg.begin + DB_ROWS - 1) / DB_ROWS;
+        before += wave_sum(j < e ? n : 0);
+        if (e < base + WAVE) *own = __shfl(n, e - base, WAVE);
+    }
+    return before;
+}
 
 template <typename T>
-__global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, int splits, float* __restrict__ part)
+__global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, float* __restrict__ part)
 {
     __shared__ float sh[DB_GROUPS][DB_COLS];
-    const int e = blockIdx.y, sp = blockIdx.z, cv = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int cv = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int n = blockIdx.x * DB_COLS + 8 * cv;
+    // range blockIdx.y of the experts' consecutive ranges
+    int e = -1, first = 0, before = 0;
+    for (int base = 0; base < g.E && e < 0; base += WAVE) {
+        const int j = base + lane_id();
+        const Segment sg = j < g.E ? segment_of(g.offsets, j, g.M) : Segment{0, 0};
+        const int k = (sg.end - sg.begin + DB_ROWS - 1) / DB_ROWS, excl = wave_excl_scan(k) + before;
+        const int at = (int)blockIdx.y;
+        const uint64_t hit = ballot(at >= excl && at < excl + k);
+        if (hit) {
+            const int src = (int)__builtin_ctzll(hit);
+            e = base + src;
+            first = at - __shfl(excl, src, WAVE);
+        }
+        before = __shfl(excl + k, WAVE - 1, WAVE);
+    }
+    if (e < 0) return;  // uniform
     const Segment seg = segment_of(g.offsets, e, g.M);
-    const int len = seg.end - seg.begin, per = (len + splits - 1) / splits;
-    const int b = seg.begin + min(sp * per, len), t = seg.begin + min((sp + 1) * per, len);
+    const int b = seg.begin + first * DB_ROWS, t = min(b + DB_ROWS, seg.end);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n < g.N) {
         const T* p = static_cast<const T*>(g.dc) + n;
-        auto row = [&](int s) {
-            return s < t ? load8_masked(p + (size_t)s * g.ldc, g.N - n) : u32x4{0, 0, 0, 0};
-        };
-        for (int s = b + grp; s < t; s += 4 * DB_GROUPS) {
-            u32x4 x[4];
+        for (int s = b + grp; s < t; s += 8 * DB_GROUPS) {
+            u32x4 x[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = row(s + DB_GROUPS * i);
+            for (int i = 0; i < 8; ++i) {
+                const int r = s + DB_GROUPS * i;
+                x[i] = r < t ? load8_masked(p + (size_t)r * g.ldc, g.N - n) : u32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[2 * j] += lo_f32<T>(x[i][j]);
@@ -735,7 +768,29 @@ __global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, int sp
     float s = sh[0][threadIdx.x];
 #pragma unroll
     for (int q = 1; q < DB_GROUPS; ++q) s += sh[q][threadIdx.x];
-    part[((size_t)sp * g.E + e) * g.N + c] = s;
+    part[(size_t)blockIdx.y * g.N + c] = s;
+}
+
+__global__ __launch_bounds__(256) void dbias_reduce_kernel(GpArgs g, const float* __restrict__ part,
+                                                           float* __restrict__ dbias)
+{
+    const int e = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+    int own = 0;
+    const int before = dbias_ranges(g, e, &own);
+    if (n >= g.N) return;
+    const float* p = part + (size_t)before * g.N + n;
+    float s = 0.f;
+    int i = 0;
+    for (; i + 8 <= own; i += 8) {  // 8 loads in flight, added in order
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = p[(size_t)(i + q) * g.N];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += x[q];
+    }
+    for (; i < own; ++i) s += p[(size_t)i * g.N];
+    float* out = dbias + (size_t)e * g.N + n;
+    *out = g.accumulate ? *out + s : s;
 }
 
 __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* __restrict__ p, long long n)
@@ -772,22 +827,17 @@ hipError_t launch_cfg(const GpArgs& g, hipStream_t s)
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool vec_stride(long long ld) { return ld % 8 == 0 && ld <= 4ll << 20; }
 
-// 320 or 256 tile rows: the one that covers the output's rows in less time.  A
-// workgroup fills a CU, so forward and dgrad run in rounds of 256 tiles (half a
-// tile more per expert for its ragged end), a round taking time in proportion
-// to the tile's rows; the weight gradient's tiles differ in length and go out
-// longest first, so there it is the rows covered that count.
+// 320 or 256 tile rows: the one that covers the output's rows with fewer, and
+// 320 where they tie (it loads a tenth less per product).  Measured on the Zipf
+// prefill, 320 / 256 rows: 5760 columns 1188 / 1224 us, gradients at 2880 x 2880
+// 1369 / 1404 us.  Counting rounds of 256 tiles instead (2592 tiles of 320 rows
+// are 10.1 of them) predicts the opposite and is wrong.
 template <int MODE>
 bool wide_tile(const GpArgs& g)
 {
     const int R = MODE == GP_FWD ? g.N : g.K;
-    auto cost = [&](int BR) {
-        const long long nt = (R + BR - 1) / BR;
-        if (MODE == GP_WGRAD) return nt * BR;
-        const long long tiles = nt * ((g.M + 255) / 256 + g.E / 2);
-        return (tiles + 255) / 256 * BR;
-    };
-    return cost(TileWide::BR) <= cost(TileLarge::BR);
+    auto covered = [&](int BR) { return (R + BR - 1) / BR * BR; };
+    return covered(TileWide::BR) <= covered(TileLarge::BR);
 }
 
 template <typename T, typename O, int MODE>
@@ -873,11 +923,8 @@ int gmm_wgrad_splits(int M, int N, int K, int E)
     return sp < 1 ? 1 : sp > 64 ? 64 : (int)sp;
 }
 
-int gmm_dbias_splits(int M, int E)
-{
-    const long long sp = (long long)M / E / 64;
-    return sp < 1 ? 1 : sp > 32 ? 32 : (int)sp;
-}
+// sum over experts of ceil(len / DB_ROWS)
+int gmm_dbias_ranges(int M, int E) { return M / DB_ROWS + E; }
 
 hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
 {
@@ -887,7 +934,19 @@ hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
     const bool vec = aligned16(a.a) && aligned16(a.dc) && a.K % 8 == 0 && a.N % 8 == 0 && vec_stride(a.lda) &&
                      vec_stride(a.ldc);
     const bool small = (long long)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E * a.splits < 256;
+    // The bias gradient first: after the weight gradient its reads would wait for
+    // that kernel's writes to drain to HBM.
     hipError_t err;
+    if (a.dbias) {
+        const dim3 grid((a.N + DB_COLS - 1) / DB_COLS, gmm_dbias_ranges(a.M, a.E));
+        if (a.dtype == DT_BF16)
+            hipLaunchKernelGGL(dbias_partial_kernel<bf16_t>, grid, dim3(DB_COLS), 0, s, g, a.dbias_part);
+        else
+            hipLaunchKernelGGL(dbias_partial_kernel<f16_t>, grid, dim3(DB_COLS), 0, s, g, a.dbias_part);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+        hipLaunchKernelGGL(dbias_reduce_kernel, dim3((a.N + 255) / 256, a.E), dim3(256), 0, s, g, a.dbias_part, a.dbias);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
     if (a.splits > 1) {
         g.out = a.part;
         g.accumulate = 0;
@@ -905,22 +964,9 @@ hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
         else
             hipLaunchKernelGGL(gmm_reduce_kernel<f16_t>, grid, dim3(256), 0, s, a.part, n, a.splits, 0,
                                static_cast<f16_t*>(a.out));
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-    } else if ((err = launch_types<GP_WGRAD>(a, g, vec, small, s)) != hipSuccess) {
-        return err;
+        return hipGetLastError();
     }
-    if (!a.dbias) return hipSuccess;
-    const int sp = gmm_dbias_splits(a.M, a.E);
-    const dim3 grid((a.N + DB_COLS - 1) / DB_COLS, a.E, sp);
-    if (a.dtype == DT_BF16)
-        hipLaunchKernelGGL(dbias_partial_kernel<bf16_t>, grid, dim3(DB_COLS), 0, s, g, sp, a.dbias_part);
-    else
-        hipLaunchKernelGGL(dbias_partial_kernel<f16_t>, grid, dim3(DB_COLS), 0, s, g, sp, a.dbias_part);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
-    const long long n = (long long)a.E * a.N;
-    hipLaunchKernelGGL(gmm_reduce_kernel<float>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.dbias_part, n,
-                       sp, a.accumulate, a.dbias);
-    return hipGetLastError();
+    return launch_types<GP_WGRAD>(a, g, vec, small, s);
 }
 
 }  // namespace moe

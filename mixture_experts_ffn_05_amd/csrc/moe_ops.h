@@ -41,9 +41,10 @@ hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s);
 // The decode form of the forward product (weights streamed once).
 hipError_t launch_gmm_skinny(const GmmArgs& a, hipStream_t s);
 bool gmm_use_skinny(const GmmArgs& a);
-// Row ranges that the weight and the bias gradient cut the segments into.
+// Row ranges that the weight gradient cuts each segment into, and that the bias
+// gradient cuts all of them into (at most).
 int gmm_wgrad_splits(int M, int N, int K, int E);
-int gmm_dbias_splits(int M, int E);
+int gmm_dbias_ranges(int M, int E);
 // n 16-bit zeros at p (null or n <= 0: nothing).  A kernel, not a memset, so
 // that it may be captured into a graph.
 hipError_t launch_zero16(void* p, int64_t n, hipStream_t s);

@@ -48,9 +48,10 @@ int check_rows(int M, int N, int K, int E, int T, int k)
     if (M < 0 || N <= 0 || K <= 0 || E <= 0 || T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || k > kMaxTopK || N > kMaxWidth || K > kMaxWidth) return MOE_ERR_UNSUPPORTED;
     if ((int64_t)E * N * K > (int64_t)1 << 37) return MOE_ERR_UNSUPPORTED;
-    // tiles of the smallest tile (128 x 64), as grid sizes
+    // grid sizes, for the smallest tile (128 x 64); the bias gradient's rows of workgroups
     const int64_t wide = (N > K ? N : K) / 64 + 1;
     if (wide * ((int64_t)M / 64 + E + 1) > INT32_MAX - 16) return MOE_ERR_UNSUPPORTED;
+    if (M / 128 + E > (1 << 24)) return MOE_ERR_UNSUPPORTED;
     if (((int64_t)N / 64 + 1) * ((int64_t)K / 128 + 2) * E * 64 > INT32_MAX - 16) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
@@ -108,7 +109,7 @@ WgradLayout wgrad_layout(const moe_gmm& g)
     const int sp = moe::gmm_wgrad_splits(g.M, g.N, g.K, g.E);
     L.part = 0;
     L.dbias = align_up(sp > 1 ? (size_t)sp * g.E * g.N * g.K * 4 : 0);
-    L.total = L.dbias + align_up((size_t)moe::gmm_dbias_splits(g.M, g.E) * g.E * g.N * 4);
+    L.total = L.dbias + align_up((size_t)moe::gmm_dbias_ranges(g.M, g.E) * g.N * 4);
     return L;
 }
 
