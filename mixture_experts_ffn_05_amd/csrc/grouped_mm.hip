@@ -182,21 +182,6 @@ __device__ __forceinline__ u32x4 load8_masked(const T* p, int left)
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-// Order of a half stage: NQ LDS reads, then for every block row its NM MFMAs and
-// the NP reads that replace its operand.
-template <int NQ, int NM, int NP, int... I>
-__device__ __forceinline__ void gp_order(std::integer_sequence<int, I...>)
-{
-    __builtin_amdgcn_sched_group_barrier(0x100, NQ, 0);
-    (
-        [] {
-            constexpr int reads = I >= 0 ? NP : 0;
-            __builtin_amdgcn_sched_group_barrier(0x008, NM, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-        }(),
-        ...);
-}
-
 template <typename F, int... I>
 __device__ __forceinline__ void for_constants(F f, std::integer_sequence<int, I...>)
 {
@@ -214,6 +199,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     // last of them is the first waves' only.
     constexpr int NLP = BR * 64 / 1024, DLP = (NLP + NW - 1) / NW, DLQ = BC * 64 / 1024 / NW;
     constexpr int FULL = NLP - (DLP - 1) * NW;  // waves with DLP loads
+    static_assert(2 * WB >= DLP + DLQ, "every load has its place among the MFMAs");
     static_assert(BR * 64 % 1024 == 0 && BC * 64 % (1024 * NW) == 0, "a stage is whole loads");
     __shared__ __attribute__((aligned(16))) uint8_t shp[GP_NBUF][BR * 64];
     __shared__ __attribute__((aligned(16))) uint8_t shq[GP_NBUF][BC * 64];
@@ -238,6 +224,8 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         e = gp_ranked_expert(g, er / g.splits);
         if (e < 0) return;
     } else {
+        // Blocks are dealt round-robin over the 8 XCDs; each XCD takes one
+        // contiguous run of the tile order.
         const int total = gp_total<BC>(g, nt);
         const int per = (total + 7) / 8;
         if ((int)(blockIdx.x / 8) >= per) return;
@@ -315,7 +303,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             for (int i = 0; i < DLP; ++i) {
                 const int first = st * GP_BK + 1024 * (wave + NW * i) / PRB;  // uniform
 #pragma unroll
-                for (int q = 0; q < PROWS; ++q) prow[i][q] = ids[seg.begin + j0 + min(first + q, J - 1)];
+                for (int q = 0; q < PROWS; ++q) prow[i][q] = ids[__builtin_amdgcn_readfirstlane(seg.begin + j0 + min(first + q, J - 1))];
             }
         }
     };
@@ -339,9 +327,11 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             int r = seg.begin + j0 + j;
             if constexpr (GATHER) {
                 const int sub = row - 1024 * (wave + NW * i) / PRB;
-                int p = prow[i][0];
+                // read lane by lane: a plain choice among the array's elements
+                // becomes an indexed load, and the array memory
+                int p = __builtin_amdgcn_readfirstlane(prow[i][0]);
 #pragma unroll
-                for (int q = 1; q < PROWS; ++q) p = sub == q ? prow[i][q] : p;
+                for (int q = 1; q < PROWS; ++q) p = sub == q ? __builtin_amdgcn_readfirstlane(prow[i][q]) : p;
                 r = input_row(g, p);
             }
             return pick(ok & ((unsigned)r < (unsigned)g.a_rows), A + (long long)r * g.lda + col);
@@ -416,31 +406,24 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         }
     }
     const uint32_t lds_p = lds_address(shp[0]) + 1024 * wave, lds_q = lds_address(shq[0]) + 1024 * wave;
-    // A whole stage st into buffer BUF.
-    auto issue = [&](auto buf_c, int st) {
-        constexpr int BUF = decltype(buf_c)::value;
-        const T* pb = pbase + st * pstep;
-        const T* qb = qbase + st * qstep;
-        for_constants(
-            [&](auto i_c) {
-                constexpr int i = decltype(i_c)::value, at = BUF * BR * 64 + 1024 * NW * i;
-                if (FULL < NW && i == DLP - 1 && !all_p) return;  // uniform
-                if constexpr (GATHER)
-                    dma16_at<at>(p_at(i, st), lds_p);
-                else
-                    dma16_at<at>(pb, poff[i], lds_p);
-            },
-            std::make_integer_sequence<int, DLP>{});
-        for_constants(
-            [&](auto i_c) {
-                constexpr int i = decltype(i_c)::value, at = BUF * BC * 64 + 1024 * NW * i;
-                if constexpr (Q64)
-                    dma16_at<at>(qptr[i] + st * GP_BK, lds_q);
-                else
-                    dma16_at<at>(qb, qoff[i], lds_q);
-            },
-            std::make_integer_sequence<int, DLQ>{});
-        load_rows(st + 1);
+    // Load i (P's, then Q's) of the whole stage whose bases are pb, qb and that
+    // goes to buffer BUF.
+    auto issue = [&](auto buf_c, auto i_c, int st, const T* pb, const T* qb) {
+        constexpr int BUF = decltype(buf_c)::value, n = decltype(i_c)::value;
+        if constexpr (n < DLP) {
+            constexpr int at = BUF * BR * 64 + 1024 * NW * n;
+            if (FULL < NW && n == DLP - 1 && !all_p) return;  // uniform
+            if constexpr (GATHER)
+                dma16_at<at>(p_at(n, st), lds_p);
+            else
+                dma16_at<at>(pb, poff[n], lds_p);
+        } else {
+            constexpr int i = n - DLP, at = BUF * BC * 64 + 1024 * NW * i;
+            if constexpr (Q64)
+                dma16_at<at>(qptr[i] + st * GP_BK, lds_q);
+            else
+                dma16_at<at>(qb, qoff[i], lds_q);
+        }
     };
     // Any stage, bounds checked; past the last one zeros.
     auto issue_any = [&](int st) {
@@ -522,16 +505,19 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     // The MFMAs of step s, with the fragments of the next step (1 - s of buffer
     // `next`) read among them: q into its other set first, p[m] in place once
     // its own MFMAs are issued.
-    auto step = [&](auto s_c, int next) {
+    auto step = [&](auto s_c, int next, auto between) {
         constexpr int S = decltype(s_c)::value;
         load_q(next, 1 - S);
+        for_constants(
+            [&](auto m_c) {
+                constexpr int m = decltype(m_c)::value;
 #pragma unroll
-        for (int m = 0; m < WB; ++m) {
-#pragma unroll
-            for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(p[m], q[S][t], acc[m][t], T{});
-            load_p(next, 1 - S, m);
-        }
-        gp_order<TB*(Q_TR ? 2 : 1), TB, P_TR ? 2 : 1>(std::make_integer_sequence<int, WB>{});
+                for (int t = 0; t < TB; ++t) acc[m][t] = mfma32_t(p[m], q[S][t], acc[m][t], T{});
+                load_p(next, 1 - S, m);
+                between(m_c);
+                __builtin_amdgcn_sched_barrier(0);
+            },
+            std::make_integer_sequence<int, WB>{});
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
@@ -542,7 +528,10 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         load_rows(0);
         if constexpr (VEC) {
             for (int st = 0; st < 3; ++st) issue_any(st);
-            dma_wait<0>();
+            if (FULL == NW || all_p)  // stage 0
+                dma_wait<2 * (DLP + DLQ)>();
+            else
+                dma_wait<2 * (DLP + DLQ - 1)>();
         } else {
             fetch(0, 0);
             fetch(1, 1);
@@ -557,10 +546,13 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
 #pragma unroll
             for (int m = 0; m < WB; ++m) load_p(0, 0, m);
         }
-        // Stage st in buffer buf; `load` starts the loads that follow the barrier.
-        auto stage = [&](int buf, int next, auto load) {
+        auto none = [](auto) {};
+        // Stage st in buffer buf.  After the barrier `load` runs, and `among(m)`
+        // with the MFMAs of block row m: loads given out all at once after a
+        // barrier hold up eight waves' MFMAs behind the address unit.
+        auto stage = [&](int buf, int next, auto load, auto among) {
             __builtin_amdgcn_sched_barrier(0);
-            if (live) step(S0{}, buf);
+            if (live) step(S0{}, buf, none);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (VEC) {  // stage st+1 has landed; st+2's loads may be in flight
                 if (FULL == NW || all_p)
@@ -571,7 +563,10 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             lds_barrier();  // stage st+1 visible; the buffer of stage st-1 is free
             load();
             __builtin_amdgcn_sched_barrier(0);
-            if (live) step(S1{}, next);
+            if (live)
+                step(S1{}, next, among);
+            else
+                for_constants(among, std::make_integer_sequence<int, WB>{});
         };
         int st = 0;
         if constexpr (VEC) {  // while the stages to load are whole: four at a time, buffers constant
@@ -579,18 +574,31 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
                 for_constants(
                     [&](auto b_c) {
                         constexpr int BUF = decltype(b_c)::value;
-                        stage(BUF, (BUF + 1) % GP_NBUF,
-                              [&] { issue(std::integral_constant<int, (BUF + 3) % GP_NBUF>{}, st + BUF + 3); });
+                        const int ls = st + BUF + 3;
+                        const T* pb = pbase + ls * pstep;
+                        const T* qb = qbase + ls * qstep;
+                        stage(BUF, (BUF + 1) % GP_NBUF, [] {},
+                              [&](auto m_c) {  // loads m, m + WB, ...
+                                  constexpr int m = decltype(m_c)::value;
+                                  using Buf = std::integral_constant<int, (BUF + 3) % GP_NBUF>;
+                                  if constexpr (m < DLP + DLQ) issue(Buf{}, m_c, ls, pb, qb);
+                                  if constexpr (m + WB < DLP + DLQ)
+                                      issue(Buf{}, std::integral_constant<int, m + WB>{}, ls, pb, qb);
+                                  if constexpr (m == WB - 1) load_rows(ls + 1);  // all of this stage's are issued
+                              });
                     },
                     std::make_integer_sequence<int, 4>{});
-            for (; st + 1 < nstages; ++st) stage(st % GP_NBUF, (st + 1) % GP_NBUF, [&] { issue_any(st + 3); });
+            for (; st + 1 < nstages; ++st) stage(st % GP_NBUF, (st + 1) % GP_NBUF, [&] { issue_any(st + 3); }, none);
         } else {
             auto pair = [&](int s, auto set_c) {  // set_c = s & 1, a constant so that the sets stay in registers
                 constexpr int SET = decltype(set_c)::value;
-                stage(s % GP_NBUF, (s + 1) % GP_NBUF, [&] {
-                    store(SET, (s + 2) % GP_NBUF);
-                    fetch(SET, s + 4);
-                });
+                stage(
+                    s % GP_NBUF, (s + 1) % GP_NBUF,
+                    [&] {
+                        store(SET, (s + 2) % GP_NBUF);
+                        fetch(SET, s + 4);
+                    },
+                    none);
             };
             for (; st + 2 < nstages; st += 2) {
                 pair(st, S0{});
@@ -603,7 +611,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         }
         __builtin_amdgcn_sched_barrier(0);
         if (live) {
-            step(S0{}, st % GP_NBUF);
+            step(S0{}, st % GP_NBUF, none);
 #pragma unroll
             for (int m = 0; m < WB; ++m)
 #pragma unroll
