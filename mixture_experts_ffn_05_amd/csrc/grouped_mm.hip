@@ -199,7 +199,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     // last of them is the first waves' only.
     constexpr int NLP = BR * 64 / 1024, DLP = (NLP + NW - 1) / NW, DLQ = BC * 64 / 1024 / NW;
     constexpr int FULL = NLP - (DLP - 1) * NW;  // waves with DLP loads
-    static_assert(2 * WB >= DLP + DLQ, "every load has its place among the MFMAs");
+    static_assert(WB >= DLP && WB >= DLQ, "every load has its place among the MFMAs");
     static_assert(BR * 64 % 1024 == 0 && BC * 64 % (1024 * NW) == 0, "a stage is whole loads");
     __shared__ __attribute__((aligned(16))) uint8_t shp[GP_NBUF][BR * 64];
     __shared__ __attribute__((aligned(16))) uint8_t shq[GP_NBUF][BC * 64];
@@ -406,24 +406,45 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
         }
     }
     const uint32_t lds_p = lds_address(shp[0]) + 1024 * wave, lds_q = lds_address(shq[0]) + 1024 * wave;
-    // Load i (P's, then Q's) of the whole stage whose bases are pb, qb and that
-    // goes to buffer BUF.
-    auto issue = [&](auto buf_c, auto i_c, int st, const T* pb, const T* qb) {
-        constexpr int BUF = decltype(buf_c)::value, n = decltype(i_c)::value;
-        if constexpr (n < DLP) {
-            constexpr int at = BUF * BR * 64 + 1024 * NW * n;
-            if (FULL < NW && n == DLP - 1 && !all_p) return;  // uniform
-            if constexpr (GATHER)
-                dma16_at<at>(p_at(n, st), lds_p);
-            else
-                dma16_at<at>(pb, poff[n], lds_p);
-        } else {
-            constexpr int i = n - DLP, at = BUF * BC * 64 + 1024 * NW * i;
-            if constexpr (Q64)
-                dma16_at<at>(qptr[i] + st * GP_BK, lds_q);
-            else
-                dma16_at<at>(qb, qoff[i], lds_q);
-        }
+    // P's load i, Q's load i of the whole stage st into buffer BUF.
+    auto issue_p = [&](auto buf_c, auto i_c, int st) {
+        constexpr int BUF = decltype(buf_c)::value, i = decltype(i_c)::value, at = BUF * BR * 64 + 1024 * NW * i;
+        if (FULL < NW && i == DLP - 1 && !all_p) return;  // uniform
+        if constexpr (GATHER)
+            dma16_at<at>(p_at(i, st), lds_p);
+        else
+            dma16_at<at>(pbase + st * pstep, poff[i], lds_p);
+    };
+    auto issue_q = [&](auto buf_c, auto i_c, int st) {
+        constexpr int BUF = decltype(buf_c)::value, i = decltype(i_c)::value, at = BUF * BC * 64 + 1024 * NW * i;
+        if constexpr (Q64)
+            dma16_at<at>(qptr[i] + st * GP_BK, lds_q);
+        else
+            dma16_at<at>(qbase + st * qstep, qoff[i], lds_q);
+    };
+    // The loads that go with block row m's MFMAs: P's spread over the second
+    // half of a stage, Q's over the first half of the next one.  (All at once
+    // after the barrier, eight waves' MFMAs wait behind the address unit.)
+    auto among_p = [&](auto buf_c, int st) {
+        return [&, buf_c, st](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            for_constants(
+                [&](auto i_c) {
+                    if constexpr (decltype(i_c)::value * WB / DLP == m) issue_p(buf_c, i_c, st);
+                },
+                std::make_integer_sequence<int, DLP>{});
+            if constexpr (m == WB - 1) load_rows(st + 1);
+        };
+    };
+    auto among_q = [&](auto buf_c, int st) {
+        return [&, buf_c, st](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            for_constants(
+                [&](auto i_c) {
+                    if constexpr (decltype(i_c)::value * WB / DLQ == m) issue_q(buf_c, i_c, st);
+                },
+                std::make_integer_sequence<int, DLQ>{});
+        };
     };
     // Any stage, bounds checked; past the last one zeros.
     auto issue_any = [&](int st) {
@@ -525,13 +546,18 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
     // ---- software pipeline: each stage is two 16-wide steps; the barrier that
     // publishes stage st+1 sits between them.
     if (nstages > 0) {
+        // Stages st with st + 6 < nwhole run four at a time, buffers constant,
+        // on whole stages only; the others check every bound.
+        const bool main_loop = VEC && 6 < nwhole;
         load_rows(0);
         if constexpr (VEC) {
-            for (int st = 0; st < 3; ++st) issue_any(st);
-            if (FULL == NW || all_p)  // stage 0
-                dma_wait<2 * (DLP + DLQ)>();
+            issue_any(0);
+            issue_any(1);
+            if (main_loop)
+                for_constants(among_p(std::integral_constant<int, 2>{}, 2), std::make_integer_sequence<int, WB>{});
             else
-                dma_wait<2 * (DLP + DLQ - 1)>();
+                issue_any(2);
+            dma_wait<DLP + DLQ>();  // stage 0
         } else {
             fetch(0, 0);
             fetch(1, 1);
@@ -547,12 +573,14 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             for (int m = 0; m < WB; ++m) load_p(0, 0, m);
         }
         auto none = [](auto) {};
-        // Stage st in buffer buf.  After the barrier `load` runs, and `among(m)`
-        // with the MFMAs of block row m: loads given out all at once after a
-        // barrier hold up eight waves' MFMAs behind the address unit.
-        auto stage = [&](int buf, int next, auto load, auto among) {
+        // Stage st in buffer buf.  `load` runs after the barrier, first(m) and
+        // second(m) with block row m's MFMAs before and after it.
+        auto stage = [&](int buf, int next, auto load, auto first, auto second) {
             __builtin_amdgcn_sched_barrier(0);
-            if (live) step(S0{}, buf, none);
+            if (live)
+                step(S0{}, buf, first);
+            else
+                for_constants(first, std::make_integer_sequence<int, WB>{});
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (VEC) {  // stage st+1 has landed; st+2's loads may be in flight
                 if (FULL == NW || all_p)
@@ -564,31 +592,27 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
             load();
             __builtin_amdgcn_sched_barrier(0);
             if (live)
-                step(S1{}, next, among);
+                step(S1{}, next, second);
             else
-                for_constants(among, std::make_integer_sequence<int, WB>{});
+                for_constants(second, std::make_integer_sequence<int, WB>{});
         };
         int st = 0;
-        if constexpr (VEC) {  // while the stages to load are whole: four at a time, buffers constant
-            for (; st + 6 < nwhole; st += 4)
-                for_constants(
-                    [&](auto b_c) {
-                        constexpr int BUF = decltype(b_c)::value;
-                        const int ls = st + BUF + 3;
-                        const T* pb = pbase + ls * pstep;
-                        const T* qb = qbase + ls * qstep;
-                        stage(BUF, (BUF + 1) % GP_NBUF, [] {},
-                              [&](auto m_c) {  // loads m, m + WB, ...
-                                  constexpr int m = decltype(m_c)::value;
-                                  using Buf = std::integral_constant<int, (BUF + 3) % GP_NBUF>;
-                                  if constexpr (m < DLP + DLQ) issue(Buf{}, m_c, ls, pb, qb);
-                                  if constexpr (m + WB < DLP + DLQ)
-                                      issue(Buf{}, std::integral_constant<int, m + WB>{}, ls, pb, qb);
-                                  if constexpr (m == WB - 1) load_rows(ls + 1);  // all of this stage's are issued
-                              });
-                    },
-                    std::make_integer_sequence<int, 4>{});
-            for (; st + 1 < nstages; ++st) stage(st % GP_NBUF, (st + 1) % GP_NBUF, [&] { issue_any(st + 3); }, none);
+        if constexpr (VEC) {
+            if (main_loop) {
+                for (; st + 6 < nwhole; st += 4)
+                    for_constants(
+                        [&](auto b_c) {
+                            constexpr int BUF = decltype(b_c)::value;
+                            stage(BUF, (BUF + 1) % GP_NBUF, [] {},
+                                  among_q(std::integral_constant<int, (BUF + 2) % GP_NBUF>{}, st + BUF + 2),
+                                  among_p(std::integral_constant<int, (BUF + 3) % GP_NBUF>{}, st + BUF + 3));
+                        },
+                        std::make_integer_sequence<int, 4>{});
+                // Q's of the last stage begun (st is a multiple of 4)
+                for_constants(among_q(std::integral_constant<int, 2>{}, st + 2), std::make_integer_sequence<int, WB>{});
+            }
+            for (; st + 1 < nstages; ++st)
+                stage(st % GP_NBUF, (st + 1) % GP_NBUF, [&] { issue_any(st + 3); }, none, none);
         } else {
             auto pair = [&](int s, auto set_c) {  // set_c = s & 1, a constant so that the sets stay in registers
                 constexpr int SET = decltype(set_c)::value;
@@ -598,7 +622,7 @@ __global__ __launch_bounds__(Cfg::THREADS, Cfg::THREADS / 256) void gmm_kernel(G
                         store(SET, (s + 2) % GP_NBUF);
                         fetch(SET, s + 4);
                     },
-                    none);
+                    none, none);
             };
             for (; st + 2 < nstages; st += 2) {
                 pair(st, S0{});
