@@ -263,17 +263,25 @@ class _DTypes:
 DTYPE = _DTypes()
 
 
-def _on_device(*tensors):
-    """The stream the call goes to by default is the current device's: refuse
-    tensors that live elsewhere (they would be reached, if at all, over a link
-    and without ordering)."""
+def _stream_for(stream, *tensors):
+    """The stream of a call on these tensors: the given one, or the current one
+    of the current device.  Tensors on another device are refused: they would be
+    reached over a link, if at all, and without ordering."""
     import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    dev = None
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             continue
-        if not t.is_cuda or (cur is not None and t.get_device() != cur):
-            raise ValueError(f"tensor on {t.device} while the current device is cuda:{cur}")
+        at = t.get_device()  # -1: host memory
+        if dev is None and at >= 0:
+            dev = torch.cuda.current_device()
+        if at < 0 or at != dev:
+            raise ValueError(f"tensor on {t.device}, not on the current device" + ("" if dev is None else f" (cuda:{dev})"))
+    if stream is None:
+        # the raw handle: torch.cuda.current_stream() builds an object around it,
+        # which costs more than the call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
+    return _stream(stream)
 
 
 def gmm(M: int, N: int, K: int, E: int, T: int = 0, k: int = 1, dtype: int = MOE_DT_BF16, out_dtype: int | None = None,
@@ -292,16 +300,16 @@ def norm(T: int, H: int, dtype: int = MOE_DT_BF16, wdtype: int | None = None, ki
 
 
 def moe_grouped_mm(g, a, expert_offsets, sorted_pairs, b, bias, c, stream=None):
-    _on_device(a, expert_offsets, sorted_pairs, b, bias, c)
+    st = _stream_for(stream, a, expert_offsets, sorted_pairs, b, bias, c)
     _check("moe_grouped_mm", library().moe_grouped_mm(ctypes.byref(g), _ptr(a), _ptr(expert_offsets),
                                                      _ptr(sorted_pairs), _ptr(b), _ptr(bias), _ptr(c),
-                                                     _stream(stream)))
+                                                     st))
 
 
 def moe_grouped_mm_dgrad(g, dc, expert_offsets, b, da, stream=None):
-    _on_device(dc, expert_offsets, b, da)
+    st = _stream_for(stream, dc, expert_offsets, b, da)
     _check("moe_grouped_mm_dgrad", library().moe_grouped_mm_dgrad(ctypes.byref(g), _ptr(dc), _ptr(expert_offsets),
-                                                                 _ptr(b), _ptr(da), _stream(stream)))
+                                                                 _ptr(b), _ptr(da), st))
 
 
 def moe_grouped_mm_workspace_size(g) -> int:
@@ -311,29 +319,29 @@ def moe_grouped_mm_workspace_size(g) -> int:
 
 
 def moe_grouped_mm_wgrad(g, a, expert_offsets, sorted_pairs, dc, db, dbias, ws, ws_bytes, stream=None):
-    _on_device(a, expert_offsets, sorted_pairs, dc, db, dbias, ws)
+    st = _stream_for(stream, a, expert_offsets, sorted_pairs, dc, db, dbias, ws)
     _check("moe_grouped_mm_wgrad", library().moe_grouped_mm_wgrad(ctypes.byref(g), _ptr(a), _ptr(expert_offsets),
                                                                  _ptr(sorted_pairs), _ptr(dc), _ptr(db), _ptr(dbias),
-                                                                 _ptr(ws), ws_bytes, _stream(stream)))
+                                                                 _ptr(ws), ws_bytes, st))
 
 
 def moe_w4_matvec(d, x, expert_offsets, sorted_pairs, codes, scales, zeros, bias, y, stream=None):
-    _on_device(x, expert_offsets, sorted_pairs, codes, scales, zeros, bias, y)
+    st = _stream_for(stream, x, expert_offsets, sorted_pairs, codes, scales, zeros, bias, y)
     _check("moe_w4_matvec", library().moe_w4_matvec(ctypes.byref(d), _ptr(x), _ptr(expert_offsets), _ptr(sorted_pairs),
                                                    _ptr(codes), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(y),
-                                                   _stream(stream)))
+                                                   st))
 
 
 def moe_norm_in(d, x, weight, bias, y, stream=None):
-    _on_device(x, weight, bias, y)
+    st = _stream_for(stream, x, weight, bias, y)
     _check("moe_norm_in", library().moe_norm_in(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                               _stream(stream)))
+                                               st))
 
 
 def moe_norm_out(d, f, residual, weight, bias, gate, rng, out, stream=None):
-    _on_device(f, residual, weight, bias, gate, rng, out)
+    st = _stream_for(stream, f, residual, weight, bias, gate, rng, out)
     _check("moe_norm_out", library().moe_norm_out(ctypes.byref(d), _ptr(f), _ptr(residual), _ptr(weight), _ptr(bias),
-                                                 _ptr(gate), _ptr(rng), _ptr(out), _stream(stream)))
+                                                 _ptr(gate), _ptr(rng), _ptr(out), st))
 
 
 def moe_norm_workspace_size(d) -> int:
@@ -343,18 +351,18 @@ def moe_norm_workspace_size(d) -> int:
 
 
 def moe_norm_in_backward(d, x, weight, dy, dres, dx, dweight, dbias, ws, ws_bytes, stream=None):
-    _on_device(x, weight, dy, dres, dx, dweight, dbias, ws)
+    st = _stream_for(stream, x, weight, dy, dres, dx, dweight, dbias, ws)
     _check("moe_norm_in_backward", library().moe_norm_in_backward(ctypes.byref(d), _ptr(x), _ptr(weight), _ptr(dy),
                                                                  _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias),
-                                                                 _ptr(ws), ws_bytes, _stream(stream)))
+                                                                 _ptr(ws), ws_bytes, st))
 
 
 def moe_norm_out_backward(d, f, weight, bias, gate, rng, dout, df, dweight, dbias, dgate, ws, ws_bytes, stream=None):
-    _on_device(f, weight, bias, gate, rng, dout, df, dweight, dbias, dgate, ws)
+    st = _stream_for(stream, f, weight, bias, gate, rng, dout, df, dweight, dbias, dgate, ws)
     _check("moe_norm_out_backward", library().moe_norm_out_backward(ctypes.byref(d), _ptr(f), _ptr(weight), _ptr(bias),
                                                                    _ptr(gate), _ptr(rng), _ptr(dout), _ptr(df),
                                                                    _ptr(dweight), _ptr(dbias), _ptr(dgate), _ptr(ws),
-                                                                   ws_bytes, _stream(stream)))
+                                                                   ws_bytes, st))
 
 
 __all__ = ["library", "dims", "expert_weights", "strerror", "moe_workspace_size", "moe_route", "moe_permute",

@@ -49,7 +49,7 @@ inline int nb_waves(int H)
 // number of rows but for the last.
 inline int nb_blocks(int T, int H)
 {
-    int most = 3072 / nb_waves(H);
+    int most = 12 * 256 / nb_waves(H);
     most = most < 1024 ? most : 1024;
     const int rows = (T + most - 1) / most;
     return rows ? (T + rows - 1) / rows : 0;

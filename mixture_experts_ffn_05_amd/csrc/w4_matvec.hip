@@ -6,10 +6,9 @@
 //
 // An item is 32 weight rows (for SwiGLU 16 gate rows and the matching 16 up
 // rows) times up to XR rows of x.  A wave streams its items' K in chunks of 256
-// columns through its own ring of LDS slots, filled by direct-to-LDS loads
+// (128) columns through its own ring of LDS slots, filled by direct-to-LDS loads
 // that run on into the next item: no barrier, no bubble between items, and
-// 4 KB of codes per slot always in flight.  A slot holds 128 bytes (whole
-// cache lines) of each weight row, the chunk's scales and zero points and the
+// a slot's codes always in flight.  A slot holds 128 (64) bytes of each weight row, the chunk's scales and zero points and the
 // x rows' same columns, so nothing but LDS is read in the loop.  With few items
 // (KS = 4) the 4 waves of a workgroup share an item, every fourth chunk each,
 // and add up through LDS.
@@ -38,11 +37,9 @@ namespace moe {
 
 namespace {
 
-constexpr int WQ_NW = 4;  // waves per workgroup
+constexpr int WQ_NW = 4;     // waves per workgroup
+constexpr int WQ_DEPTH = 2;  // ring slots per wave
 constexpr int WQ_THREADS = WQ_NW * WAVE;
-constexpr int WQ_CK = 256;    // columns per chunk
-constexpr int WQ_DEPTH = 2;   // ring slots per wave
-constexpr int WQ_ROWB = WQ_CK / 2;
 
 __device__ uint32_t wq_zeros[4] __attribute__((aligned(16)));  // never written
 
@@ -90,10 +87,16 @@ typedef __attribute__((address_space(4))) const int32_t* wq_cptr;  // read throu
 // x per item.  KS: waves that share an item's K.
 template <int GB, bool Z, int XR, int KS>
 struct WqShape {
-    static constexpr int GPC = 8 / GB;  // groups per chunk
-    static constexpr int WBYTES = 32 * WQ_ROWB, XBYTES = XR * 2 * WQ_CK, SBYTES = 32 * GPC * 4;
+    // Columns per chunk.  A wave that streams whole rows takes 128-byte pieces of
+    // them; with 16 rows of x, or rows shared by four waves, 64-byte pieces, whose
+    // slots leave room for two or more workgroups a CU.  64-byte against 128-byte
+    // pieces: 13.6 and 17.5 us (1 row, 2 of 32 experts, 2880 -> 5760, KS = 4),
+    // 14.6 and 21.8 us (64 rows, 2880 -> 2880).
+    static constexpr int CK = XR < 16 && KS == 1 ? 256 : 128, ROWB = CK / 2;
+    static constexpr int BPC = CK / 32, GPC = BPC / GB;  // 32-column blocks, groups per chunk
+    static constexpr int WBYTES = 32 * ROWB, XBYTES = XR * 2 * CK, SBYTES = GPC < 2 ? 256 : 32 * GPC * 4;
     static constexpr int SLOT = WBYTES + XBYTES + (Z ? 2 : 1) * SBYTES;
-    static constexpr int RING = WQ_NW * WQ_DEPTH * SLOT, RED = KS > 1 ? 2 * WQ_NW * 2 * WAVE : 1;
+    static constexpr int RING = WQ_NW * WQ_DEPTH * SLOT, RED = KS > 1 ? WQ_NW * 2 * WAVE : 1;
     // Two workgroups per CU where their LDS fits: asking for them also keeps
     // the matrix cores' results in ordinary registers.
     static constexpr int WAVES_PER_SIMD = RING + RED * 16 <= 80 * 1024 ? 2 : 1;
@@ -105,7 +108,8 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
     using S = WqShape<GB, Z, XR, KS>;
     static_assert(KS == 1 || KS == WQ_NW, "an item belongs to a wave or to a workgroup");
     constexpr int GPC = S::GPC, WBYTES = S::WBYTES, XBYTES = S::XBYTES, SBYTES = S::SBYTES, SLOT = S::SLOT;
-    constexpr int WL = WBYTES / 1024, XL = XBYTES / 1024, SL = 32 * GPC / WAVE;  // loads per slot
+    constexpr int WQ_CK = S::CK, WQ_ROWB = S::ROWB;
+    constexpr int WL = WBYTES / 1024, XL = XBYTES / 1024, SL = SBYTES / 256;  // loads per slot
     constexpr int NL = WL + XL + (Z ? 2 : 1) * SL;
     static_assert(XL >= 1 && (WQ_DEPTH - 1) * NL < 64, "load count");
     __shared__ __attribute__((aligned(16))) uint8_t sh[S::RING];
@@ -168,24 +172,26 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         return swiglu ? (i < 16 ? n : half + n) : min(t.n0 + i, g.N - 1);
     };
 
-    // ---- issue side: sources of the item being loaded.  Weights: load i
-    // covers 8 rows of 128 bytes, piece p of row r lying at p ^ (r / 2 % 8); x:
-    // 2 rows of 512 bytes, piece p of row r at p ^ (r % 16): the 16 rows that
-    // one fragment read touches fall on different banks.
+    // ---- issue side: sources of the item being loaded.  Weights: a row's chunk
+    // is WPP 16-byte pieces, piece p of row r lying at p ^ wswz(r); x: XPP pieces,
+    // piece p of row r at p ^ (r % 16): the 16 rows that one fragment read touches
+    // fall on different banks.
+    constexpr int WPP = WQ_ROWB / 16, WRPL = WAVE / WPP;        // pieces a row, rows a load
+    constexpr int XPP = 2 * WQ_CK / 16, XRPL = WAVE / XPP;
+    auto wswz = [](int r) { return WPP == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
     const uintptr_t zeros = reinterpret_cast<uintptr_t>(wq_zeros);
     uintptr_t wsrc[WL], xsrc[XL], ssrc[SL], zsrc[Z ? SL : 1];
     int xlim[XL];
-    const int wk = 32 * ((lane & 7) ^ ((lane >> 4) & 3));  // + 32 * ((4 i) & 7): row 8 i + lane / 8
     auto open = [&](const Item& t) {
         const size_t erow = (size_t)t.e * g.N;
 #pragma unroll
         for (int i = 0; i < WL; ++i) {
-            const int r = 8 * i + (lane >> 3), p = (lane & 7) ^ ((r >> 1) & 7);
+            const int r = WRPL * i + lane / WPP, p = (lane % WPP) ^ wswz(r);
             wsrc[i] = reinterpret_cast<uintptr_t>(g.codes) + (erow + wrow(t, r)) * (size_t)(g.K / 2) + 16 * p;
         }
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
-            const int q = lane + WAVE * i;
+            const int q = min(lane + WAVE * i, 32 * GPC - 1);
             const size_t at = (erow + wrow(t, q / GPC)) * G + q % GPC;
             ssrc[i] = reinterpret_cast<uintptr_t>(g.scales) + 2 * at;
             if (Z) zsrc[i] = reinterpret_cast<uintptr_t>(g.zeros) + at;
@@ -193,19 +199,19 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         wq_cptr ids = (wq_cptr)(uintptr_t)g.pairs;
 #pragma unroll
         for (int i = 0; i < XL; ++i) {
-            int row[2];
+            int src = -1;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = t.s0 + 2 * i + h;
-                row[h] = s < t.s1 ? s : -1;
+            for (int h = 0; h < XRPL; ++h) {
+                const int s = t.s0 + XRPL * i + h;
+                int row = s < t.s1 ? s : -1;
                 if (g.pairs) {  // uniform
                     const int p = ids[min(s, t.s1 - 1)];
-                    row[h] = s < t.s1 && p >= 0 ? p / g.k : -1;
+                    row = s < t.s1 && p >= 0 ? p / g.k : -1;
                 }
-                if (row[h] >= g.x_rows) row[h] = -1;
+                if (row >= g.x_rows) row = -1;
+                src = lane / XPP == h ? row : src;
             }
-            const int r = 2 * i + (lane >> 5), src = lane < 32 ? row[0] : row[1];
-            const int p = (lane & 31) ^ (r & 15);
+            const int r = XRPL * i + lane / XPP, p = (lane % XPP) ^ (r & 15);
             xlim[i] = src >= 0 ? g.K - 8 * p : 0;
             xsrc[i] = reinterpret_cast<uintptr_t>(g.x) + ((size_t)max(src, 0) * g.K + 8 * p) * 2;
         }
@@ -216,7 +222,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         const int k0 = c * WQ_CK;
 #pragma unroll
         for (int i = 0; i < WL; ++i) {
-            const int k = wk ^ (i & 1 ? 128 : 0);  // rows 8 i + ..: r / 2 % 8 differs by 4 between odd and even i
+            const int k = 32 * ((lane % WPP) ^ wswz(WRPL * i + lane / WPP));
             dma16(reinterpret_cast<const void*>(k0 + k < g.K ? wsrc[i] + (size_t)c * WQ_ROWB : zeros), at + 1024 * i);
         }
 #pragma unroll
@@ -224,7 +230,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
             dma16(reinterpret_cast<const void*>(k0 < xlim[i] ? xsrc[i] + 2 * (size_t)k0 : zeros), at + WBYTES + 1024 * i);
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
-            const bool ok = c * GPC + (lane + WAVE * i) % GPC < G;
+            const bool ok = c * GPC + min(lane + WAVE * i, 32 * GPC - 1) % GPC < G;
             dma_u16(reinterpret_cast<const void*>(ok ? ssrc[i] + 2 * (size_t)(c * GPC) : zeros),
                     at + WBYTES + XBYTES + 256 * i);
             if constexpr (Z)
@@ -267,7 +273,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
 #pragma unroll
     for (int u = 0; u < SLOTS; ++u) mask[u] = my_slot == u ? ~0u : 0u;
     const u32x4 ones = u32x4{Code16<T>::one, Code16<T>::one, Code16<T>::one, Code16<T>::one};
-    int slot = 0, parity = 0;
+    int slot = 0;
     for (; it < items; it += stride) {
         cur = locate(it);
         f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
                         for (int n = 0; n < 2; ++n) {
                             const int r = 16 * n + l16, j = (q + u) * GB + b;
                             const uint32_t w =
-                                *reinterpret_cast<const uint32_t*>(at + r * WQ_ROWB + ((j ^ ((r >> 1) & 7)) << 4) + 4 * kg);
+                                *reinterpret_cast<const uint32_t*>(at + r * WQ_ROWB + ((j ^ wswz(r)) << 4) + 4 * kg);
                             dsum[n] = mfma16_t(am, code.decode(w), dsum[n], T{});
                         }
                     }
@@ -300,7 +306,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
                 for (int n = 0; n < 2; ++n) {
                     const int si = (16 * n + l16) * GPC + q + d_slot;
                     const float sc = to_f32(T{(uint16_t)st[si]});
-                    const float z = Z ? 16.f + (float)(st[32 * GPC + si] & 15u) : 24.f;
+                    const float z = Z ? 16.f + (float)(st[SBYTES / 4 + si] & 15u) : 24.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(sc, fmaf(-z, xsum[i], dsum[n][i]), acc[n][i]);
                 }
@@ -320,19 +326,18 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
                 if constexpr (XR <= 8) acc[n][i] += __shfl_xor(acc[n][i], 32, WAVE);
                 if constexpr (XR <= 4) acc[n][i] += __shfl_xor(acc[n][i], 16, WAVE);
             }
-        if constexpr (KS > 1) {  // two buffers by turns: one barrier an item
-            f32x4* buf = red + parity * (WQ_NW * 2 * WAVE);
-            parity ^= 1;
+        if constexpr (KS > 1) {
+            if (it != (int)blockIdx.x) lds_barrier();  // the last item's sums have been read
 #pragma unroll
-            for (int n = 0; n < 2; ++n) buf[(wave * 2 + n) * WAVE + lane] = acc[n];
+            for (int n = 0; n < 2; ++n) red[(wave * 2 + n) * WAVE + lane] = acc[n];
             lds_barrier();
             if (wave >= (swiglu ? 1 : 2)) continue;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 if (!swiglu && n != wave) continue;
-                acc[n] = buf[n * WAVE + lane];
+                acc[n] = red[n * WAVE + lane];
 #pragma unroll
-                for (int w = 1; w < WQ_NW; ++w) acc[n] += buf[(w * 2 + n) * WAVE + lane];
+                for (int w = 1; w < WQ_NW; ++w) acc[n] += red[(w * 2 + n) * WAVE + lane];
             }
         }
         const T* bias = g.bias ? static_cast<const T*>(g.bias) + (size_t)cur.e * g.N : nullptr;
