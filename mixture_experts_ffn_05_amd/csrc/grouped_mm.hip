@@ -21,14 +21,25 @@
 // Both kinds give a lane the j values 16 s + 8 (lane / 32) + 0..7 in order, so
 // either kind can meet either in one MFMA.
 //
-// The tile loop is a ring of 4 LDS stages of 32 j: direct-to-LDS loads run
-// three stages ahead, one barrier a stage, placed after the first half of the
-// stage's MFMAs.  Loads past the contracted length, and past the matrix's
-// width in a transposed tile, read a 16-byte block of zeros, so tails cost no
-// branch and no garbage enters a product.  Rows and widths that are not
-// multiples of 8 elements (or bases not 16-byte aligned) cannot use the
-// direct loads (VEC = false): they go through registers, two stages ahead,
-// with unaligned 16-byte loads and an element loop only in a row's last chunk.
+// The tile loop is a ring of 4 LDS stages of 32 j filled by direct-to-LDS loads
+// two to three stages ahead, one barrier a stage, after the first half of the
+// stage's MFMAs.  The loads are spread among the MFMAs (issued together, eight
+// waves' MFMAs wait behind the address unit), their addresses are a uniform base
+// per stage and fixed 32-bit offsets, and the loop is unrolled by the ring so
+// that LDS addresses are constants: it holds no address arithmetic.  P's
+// fragments are replaced in place as their MFMAs are issued, Q's are double.
+// Only the last stages check bounds; what they find past the contracted length,
+// or past the matrix's width in a transposed tile, reads as zeros.
+// Rows and widths that are not multiples of 8 elements (or bases not 16-byte
+// aligned) cannot use the direct loads (VEC = false): they go through
+// registers, with unaligned 16-byte loads and an element loop only in a row's
+// last chunk.
+//
+// Bound by the matrix cores at the clock that their load allows: 1116 us for
+// 32768 rows, 32 experts of Zipf shares, 2880 -> 5760 bf16 (0.97 PFLOP/s; the
+// library's dense product of those sizes 1.23), 1289 us for both gradients at
+// 2880 x 2880 (0.84 PFLOP/s; dense 1.11 and 0.73).  What each part gave: loads
+// among the MFMAs 1201 -> 1125 us, no address arithmetic 1242 -> 1171.
 #include <string.h>
 
 #include <type_traits>
@@ -754,14 +765,14 @@ __global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, float*
 {
     __shared__ float sh[DB_GROUPS][DB_COLS];
     const int cv = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int n = blockIdx.x * DB_COLS + 8 * cv;
-    // range blockIdx.y of the experts' consecutive ranges
+    const int cols = (g.N + DB_COLS - 1) / DB_COLS, at = (int)(blockIdx.x / cols), c0 = (int)(blockIdx.x % cols) * DB_COLS;
+    const int n = c0 + 8 * cv;
+    // range `at` of the experts' consecutive ranges
     int e = -1, first = 0, before = 0;
     for (int base = 0; base < g.E && e < 0; base += WAVE) {
         const int j = base + lane_id();
         const Segment sg = j < g.E ? segment_of(g.offsets, j, g.M) : Segment{0, 0};
         const int k = (sg.end - sg.begin + DB_ROWS - 1) / DB_ROWS, excl = wave_excl_scan(k) + before;
-        const int at = (int)blockIdx.y;
         const uint64_t hit = ballot(at >= excl && at < excl + k);
         if (hit) {
             const int src = (int)__builtin_ctzll(hit);
@@ -795,12 +806,12 @@ __global__ __launch_bounds__(DB_COLS) void dbias_partial_kernel(GpArgs g, float*
 #pragma unroll
     for (int j = 0; j < 8; ++j) sh[grp][8 * cv + j] = v[j];
     __syncthreads();
-    const int c = blockIdx.x * DB_COLS + threadIdx.x;
+    const int c = c0 + (int)threadIdx.x;
     if (c >= g.N) return;
     float s = sh[0][threadIdx.x];
 #pragma unroll
     for (int q = 1; q < DB_GROUPS; ++q) s += sh[q][threadIdx.x];
-    part[(size_t)blockIdx.y * g.N + c] = s;
+    part[(size_t)at * g.N + c] = s;
 }
 
 __global__ __launch_bounds__(256) void dbias_reduce_kernel(GpArgs g, const float* __restrict__ part,
@@ -827,8 +838,7 @@ __global__ __launch_bounds__(256) void dbias_reduce_kernel(GpArgs g, const float
 
 __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* __restrict__ p, long long n)
 {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) p[i] = 0;
 }
 
 template <typename T, typename O, int MODE, bool VEC, bool GATHER, typename Cfg>
@@ -917,15 +927,24 @@ hipError_t launch_types(const GmmArgs& a, const GpArgs& g, bool vec, bool small,
                                  : launch_mode<f16_t, f16_t, MODE>(g, vec, small, s);
 }
 
-// The 256 x 256 tile once an expert's share of the rows can fill most of it.
-bool use_small_tile(const GmmArgs& a) { return (long long)a.M < 128ll * a.E; }
+// The large tiles once an average expert's rows fill a third of one and there
+// are tiles for a third of the CUs.  Small against large tiles, N = K = 2880
+// unless said, in us:
+//   32 experts, N 5760: 64 rows each 234 and 265, 96 rows each 311 and 271;
+//   1 expert: 2048 rows (72 large tiles) 62 and 75, 2560 rows (90) 83 and 78;
+//   8 experts: 2048 rows (72) 77 and 90, 2560 rows (90) 94 and 81.
+bool use_small_tile(const GmmArgs& a, int cols)
+{
+    return (long long)a.M < 80ll * a.E || (long long)(a.M / TileWide::BC) * ((cols + TileWide::BR - 1) / TileWide::BR) < 85;
+}
 
 }  // namespace
 
 hipError_t launch_zero16(void* p, int64_t n, hipStream_t s)
 {
     if (!p || n <= 0) return hipSuccess;
-    hipLaunchKernelGGL(zero16_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, static_cast<uint16_t*>(p),
+    const long long blocks = (n + 255) / 256;
+    hipLaunchKernelGGL(zero16_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, static_cast<uint16_t*>(p),
                        (long long)n);
     return hipGetLastError();
 }
@@ -934,23 +953,28 @@ hipError_t launch_gmm_forward(const GmmArgs& a, hipStream_t s)
 {
     const GpArgs g = gp_args(a);
     const bool vec = aligned16(a.a) && aligned16(a.b) && a.K % 8 == 0 && vec_stride(a.lda);
-    return launch_types<GP_FWD>(a, g, vec, use_small_tile(a), s);
+    return launch_types<GP_FWD>(a, g, vec, use_small_tile(a, a.N), s);
 }
 
 hipError_t launch_gmm_dgrad(const GmmArgs& a, hipStream_t s)
 {
     const GpArgs g = gp_args(a);
     const bool vec = aligned16(a.dc) && aligned16(a.b) && a.K % 8 == 0 && a.N % 8 == 0 && vec_stride(a.ldc);
-    return launch_types<GP_DGRAD>(a, g, vec, use_small_tile(a), s);
+    return launch_types<GP_DGRAD>(a, g, vec, use_small_tile(a, a.K), s);
 }
 
+// Ranges of rows whose partial sums are added up afterwards, where the small
+// tiles alone would leave CUs without work: two tiles per CU, and at least 1024
+// rows of an average expert per range.  Without and with, one expert, N = K =
+// 1024 (128 tiles), in us: 2048 rows 14.4 and 15.9, 4096 rows 32 and 22, 65536
+// rows 457 and 231.  From 256 tiles on the second pass costs more than it gives:
+// 8 experts, N = K = 512, 65536 rows, 67 without and 79 with two ranges.
 int gmm_wgrad_splits(int M, int N, int K, int E)
 {
-    const long long tiles = (long long)((N + 255) / 256) * ((K + 255) / 256) * E;
+    const long long tiles = (long long)((N + TileSmall::BR - 1) / TileSmall::BR) *
+                            ((K + TileSmall::BC - 1) / TileSmall::BC) * E;
     if (tiles >= 256) return 1;
-    // at least 512 rows of an average expert per range: below that the extra
-    // pass over the partial sums costs more than the shorter loops give
-    const long long by_rows = (long long)M / E / 512, by_tiles = 256 / tiles;
+    const long long by_rows = (long long)M / E / 1024, by_tiles = 512 / tiles;
     const long long sp = by_rows < by_tiles ? by_rows : by_tiles;
     return sp < 1 ? 1 : sp > 64 ? 64 : (int)sp;
 }
@@ -965,12 +989,16 @@ hipError_t launch_gmm_wgrad(const GmmArgs& a, hipStream_t s)
     g.accumulate = a.accumulate;
     const bool vec = aligned16(a.a) && aligned16(a.dc) && a.K % 8 == 0 && a.N % 8 == 0 && vec_stride(a.lda) &&
                      vec_stride(a.ldc);
+    // The large tiles once every CU has one.  Small against large, in us: 4096
+    // rows, 2 experts, 2880 x 2880 (288 large tiles) 91 and 71; 8192 rows, 8
+    // experts, 1024 x 2048 (256) 52 and 42; 1 expert, 2880 x 2880 (144) 180 and 191.
     const bool small = (long long)((a.N + 255) / 256) * ((a.K + 255) / 256) * a.E * a.splits < 256;
     // The bias gradient first: after the weight gradient its reads would wait for
     // that kernel's writes to drain to HBM.
     hipError_t err;
     if (a.dbias) {
-        const dim3 grid((a.N + DB_COLS - 1) / DB_COLS, gmm_dbias_ranges(a.M, a.E));
+        const int cols = (a.N + DB_COLS - 1) / DB_COLS;
+        const dim3 grid((unsigned)((long long)cols * gmm_dbias_ranges(a.M, a.E)));
         if (a.dtype == DT_BF16)
             hipLaunchKernelGGL(dbias_partial_kernel<bf16_t>, grid, dim3(DB_COLS), 0, s, g, a.dbias_part);
         else

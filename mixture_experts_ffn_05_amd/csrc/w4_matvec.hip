@@ -379,8 +379,11 @@ hipError_t launch_xr(const WqArgs& g, hipStream_t s)
 {
     const long long tiles = g.swiglu ? (g.N / 2 + 15) / 16 : (g.N + 31) / 32;
     const long long items = tiles * ((g.M + XR - 1) / XR + (g.E == 1 ? 0 : g.E < g.M ? g.E : g.M));  // at most
-    // A wave per item once there are items for every wave of the chip twice over.
-    if (items >= 2 * 8 * WQ_CUS) {
+    // A wave per item once there are items for every wave of the chip (two workgroups a CU),
+    // a workgroup per item before.  Wave and workgroup, 2880 columns, in us: 1 row,
+    // 90 items 16 and 8, 1024 items 18 and 15, 2048 items 26 and 28; 32 experts'
+    // SwiGLU, 4 of them 17 and 13, 16 of them (2880 items) 32 and 35.
+    if (items >= 8 * WQ_CUS) {
         const long long blocks = (items + WQ_NW - 1) / WQ_NW, most = 2 * WQ_CUS;
         hipLaunchKernelGGL((w4_matvec_kernel<T, GB, Z, XR, 1>), dim3((unsigned)(blocks < most ? blocks : most)),
                            dim3(WQ_THREADS), 0, s, g);
@@ -392,7 +395,9 @@ hipError_t launch_xr(const WqArgs& g, hipStream_t s)
 
 // Rows of x per item: twice an expert's average share (its share varies), so
 // that a second pass over an expert's codes is rare, in the smallest form that
-// holds them; a wider one costs LDS space, and with it loads in flight.
+// holds them; a wider one costs LDS space, and with it loads in flight.  32
+// experts' SwiGLU, 2880 -> 5760, in us: 2 rows each, 67 with 4 and 82 with 16; 4
+// rows each, 70, 72 and 85 with 4, 8 and 16; 8 rows each, 114 with 4 and 90 with 16.
 template <typename T, int GB, bool Z>
 hipError_t launch_rows(const WqArgs& g, hipStream_t s)
 {
