@@ -8,9 +8,11 @@
 // squared differences from the mean, a second pass over registers).  Bound by
 // HBM: 2 rows moved per row of norm_in, 3 (4 with a full gate) of norm_out.
 //
-// A row is held by one wave up to 4096 columns (no barrier, rows independent,
-// 4 of them in a workgroup), by 256 threads above, each
-// thread keeping vectors of 8 columns (16 bytes), lanes adjacent.  Rows of odd
+// A row is held by one wave up to 2048 columns (no barrier, rows independent, 4
+// of them in a workgroup), by 256 threads above, each thread keeping vectors of
+// 8 columns (16 bytes), lanes adjacent.  norm_in with a wave and with 256 threads
+// a row, bf16, in us: 8192 x 512 5.1 and 8.6, 8192 x 2048 12.4 and 14.1, 1024 x 2880
+// 5.6 and 4.8, 8192 x 2880 19.6 and 19.1, 4096 x 4096 13.5 and 12.5.  Rows of odd
 // length use unaligned vector accesses and an element loop in the last vector.
 #include "norm_device.h"
 
@@ -126,8 +128,7 @@ hipError_t launch_type(const NormArgs& a, hipStream_t s)
     MOE_NORM_LAUNCH(64, 1)
     MOE_NORM_LAUNCH(64, 2)
     MOE_NORM_LAUNCH(64, 4)
-    MOE_NORM_LAUNCH(64, 6)
-    MOE_NORM_LAUNCH(64, 8)
+    MOE_NORM_LAUNCH(256, 2)
     MOE_NORM_LAUNCH(256, 4)
     MOE_NORM_LAUNCH(256, 8)
 #undef MOE_NORM_LAUNCH
