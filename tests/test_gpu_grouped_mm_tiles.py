@@ -1,0 +1,88 @@
+"""The grouped products at sizes that take the large tiles (320 and 256 rows of
+the output's width) and the row ranges of the weight gradient, against their
+64-bit forms: segments that end inside tiles, empty ones, rows outside, pairs."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import mixture_experts_ffn_05_amd as moe
+from tests import operators_reference as ref
+from tests.test_gpu_grouped_mm import DT, _case, _put, _strided
+
+pytestmark = pytest.mark.gpu
+
+# Forward and data gradient: 43 tiles of 256 rows times 2 of the width, and 80
+# rows an expert, make the large tiles.  One width of 600 (320-wide tiles cover
+# it with fewer), one of 504 (256-wide ones do).
+LARGE = {
+    "gather": dict(T=3700, k=3, E=5, N=600, K=504, gather=True, empty=(2,), bad_pairs=True),
+    "rows": dict(T=11100, k=1, E=3, N=504, K=600, gather=False, lead=19, behind=45),
+    "dense": dict(T=11008, k=1, E=1, N=640, K=352, gather=False),
+    "many_experts": dict(T=3100, k=4, E=130, N=600, K=72, gather=True, empty=tuple(range(0, 130, 7))),
+}
+
+
+@pytest.mark.parametrize("name,dtype", [("gather", "bf16"), ("rows", "bf16"), ("rows", "f16"), ("dense", "f16"),
+                                       ("many_experts", "bf16")])
+def test_large_tiles(name, dtype):
+    print(f"large tiles {name} {dtype}", flush=True)
+    c = dict(LARGE[name])
+    N, K, E = c["N"], c["K"], c["E"]
+    a, b, bias, dc, off, pairs, M = _case(31, dtype, **c)
+    lda, ldc = K + 8, N + 16  # rows with room behind them
+    for out in (dtype, "f32"):
+        d = moe.gmm(M, N, K, E, T=c["T"], k=c["k"], dtype=moe.DTYPE[DT[dtype]], out_dtype=moe.DTYPE[DT[out]], lda=lda, ldc=ldc)
+        y = torch.full((M, ldc), 7.0, dtype=DT[out], device="cuda")
+        moe.moe_grouped_mm(d, _strided(a, lda).cuda(), _put(off), _put(pairs), _put(b), _put(bias), y)
+        da = torch.full((M, lda), 7.0, dtype=DT[out], device="cuda")
+        moe.moe_grouped_mm_dgrad(d, _strided(dc, ldc).cuda(), _put(off), _put(b), da)
+        torch.cuda.synchronize()
+        y, da = y.cpu(), da.cpu()
+        want, bound, inside = ref.product(a, off, pairs, c["k"], b, bias, DT[out], M)
+        ref.assert_within(y[inside, :N], want[inside], bound[inside], f"{name} forward {dtype}->{out}")
+        assert (y[~inside] == 7).all() and (y[:, N:] == 7).all()
+        want, bound, inside = ref.product_dgrad(dc, off, b, DT[out], M)
+        ref.assert_within(da[inside, :K], want[inside], bound[inside], f"{name} dgrad {dtype}->{out}")
+        assert (da[~inside] == 7).all() and (da[:, K:] == 7).all()
+
+
+WGRAD = {
+    # 256 large tiles or more, of 320 and of 256 columns of `a`
+    "wide": dict(T=1500, k=1, E=64, N=520, K=304, gather=True, empty=(0, 17, 63), bad_pairs=True),
+    "large": dict(T=700, k=2, E=90, N=264, K=504, gather=True, empty=tuple(range(3, 90, 9)), lead=5, behind=3),
+    "rows": dict(T=2500, k=1, E=64, N=520, K=304, gather=False),
+    # few tiles and 1024 rows an expert: cut into row ranges
+    "split_dense": dict(T=9300, k=1, E=1, N=136, K=200, gather=False),
+    "split_gather": dict(T=3500, k=2, E=3, N=72, K=64, gather=True, empty=(1,)),
+    "split_odd": dict(T=5200, k=1, E=2, N=33, K=35, gather=True, bad_pairs=True),
+    "split_outside": dict(T=4200, k=1, E=2, N=40, K=136, gather=False, lead=700, behind=900),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("name", sorted(WGRAD))
+def test_weight_gradient_tiles(name, dtype):
+    print(f"wgrad tiles {name} {dtype}", flush=True)
+    c = dict(WGRAD[name])
+    E, N, K = c["E"], c["N"], c["K"]
+    a, _, _, dc, off, pairs, M = _case(33, dtype, **c)
+    for out, accumulate in (("f32", True), (dtype, False)):
+        d = moe.gmm(M, N, K, E, T=c["T"], k=c["k"], dtype=moe.DTYPE[DT[dtype]], out_dtype=moe.DTYPE[DT[out]],
+                    accumulate=accumulate)
+        n = moe.moe_grouped_mm_workspace_size(d)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        db = torch.full((E, N, K), 0.5, dtype=DT[out], device="cuda")
+        dbias = torch.full((E, N), 0.25, dtype=torch.float32, device="cuda")
+        moe.moe_grouped_mm_wgrad(d, _put(a), _put(off), _put(pairs), _put(dc), db, dbias, ws, n)
+        torch.cuda.synchronize()
+        want, bound, wbias, bbias = ref.product_wgrad(a, off, pairs, c["k"], dc, E, DT[out], M)
+        if accumulate:
+            want, wbias = want + 0.5, wbias + 0.25
+            bound, bbias = bound + ref.U * (want.abs() + 0.5), bbias + ref.U * (wbias.abs() + 0.25)
+        ref.assert_within(db, want, bound, f"{name} db {out}")
+        ref.assert_within(dbias, wbias, bbias, f"{name} dbias {out}")
+        db2 = torch.full_like(db, 0.5)
+        moe.moe_grouped_mm_wgrad(d, _put(a), _put(off), _put(pairs), _put(dc), db2, None, ws, n)
+        torch.cuda.synchronize()
+        assert torch.equal(db, db2), "the same call gives other bits"
