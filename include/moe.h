@@ -372,9 +372,11 @@ enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 };
  * Any N, K >= 1 and any stride; pointers need only their element's alignment.
  * Rows of a, b and dc whose starts are all 16-byte aligned (K, N where it is
  * contracted or transposed, strides multiples of 8) take the fast loads.
- * Segments are read as clamped to [0, M], empty where an offset decreases;
- * rows outside every segment are left as they were, an expert without rows
- * gets zero gradients.  A sorted pair outside [0, T * k) reads a row of zeros.
+ * Segments are read as clamped to [0, M], empty where an offset decreases
+ * (rows that two segments then share, and gradients of experts behind a
+ * decrease, are unspecified; nothing outside the arrays is touched); rows
+ * outside every segment are left as they were, an expert without rows gets
+ * zero gradients.  A sorted pair outside [0, T * k) reads a row of zeros.
  * expert_offsets may be NULL when E = 1 (all M rows).  M = 0: forward and
  * dgrad do nothing, wgrad writes zeros (nothing when accumulating).
  * Errors: NULL, sizes < 1 (M, T < 0), a stride below the row's length, missing
@@ -401,7 +403,7 @@ int moe_grouped_mm_wgrad(const moe_gmm* g, const void* a, const int32_t* expert_
 
 /* Products with 4-bit integer weights and a scale per group, for few rows per
  * expert (decoding; any number of rows is right, but the weights are read
- * again for every 16 rows of an expert):
+ * again for every 4 to 16 rows of an expert):
  *   w[e][n][i] = scales[e][n][i / group] * (code - zero),
  *   v[s][n]    = sum_i x[r(s)][i] w[e][n][i] + bias[e][n],
  *   act NONE:   y[s][n] = v[s][n]                                    y [M][N]

@@ -819,7 +819,9 @@ __global__ __launch_bounds__(256) void dbias_reduce_kernel(GpArgs g, const float
 {
     const int e = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
     int own = 0;
-    const int before = dbias_ranges(g, e, &own);
+    // (offsets that decrease can count more ranges than there are: bounded)
+    const int ranges = g.M / DB_ROWS + g.E, before = min(dbias_ranges(g, e, &own), ranges);
+    own = min(own, ranges - before);
     if (n >= g.N) return;
     const float* p = part + (size_t)before * g.N + n;
     float s = 0.f;
@@ -852,7 +854,7 @@ hipError_t launch_gathered(const GpArgs& g, hipStream_t s)
         const long long nt = ((MODE == GP_FWD ? g.N : g.K) + Cfg::BR - 1) / Cfg::BR;
         grid = (nt * ((g.M + Cfg::BC - 1) / Cfg::BC + g.E) + 7) / 8 * 8;
     }
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (grid * Cfg::THREADS > 0xFFFFFFFFll) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gmm_kernel<T, O, MODE, VEC, GATHER, Cfg>), dim3((unsigned)grid), dim3(Cfg::THREADS), 0, s, g);
     return hipGetLastError();
 }

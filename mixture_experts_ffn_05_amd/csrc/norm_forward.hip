@@ -21,12 +21,13 @@ namespace moe {
 namespace {
 
 template <typename T, int TPR, int NV, bool OUT>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormArgs a)
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a)
 {
     __shared__ float lds[TPR > WAVE ? 8 : 1];
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-    const int t = blockIdx.x * RPB + (int)threadIdx.x / TPR;
-    if (t >= a.T) return;  // uniform per wave; per block where a row spans waves
+    constexpr int RPB = 256 / TPR;
+    const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + (int)threadIdx.x / TPR;
+    if (row >= a.T) return;  // uniform per wave; per block where a row spans waves
+    const int t = (int)row;
     const int v0 = threadIdx.x % TPR, H = a.H;
     const size_t at = (size_t)t * H;
     const T* xr = static_cast<const T*>(a.x) + at;
@@ -118,11 +119,12 @@ template <typename T, bool OUT>
 hipError_t launch_type(const NormArgs& a, hipStream_t s)
 {
     const int nv = (a.H + 7) / 8;
+    constexpr unsigned most = 1u << 22;  // workgroups in x: fewer than 2^32 threads
 #define MOE_NORM_LAUNCH(TPR, NV)                                                                          \
     if (nv <= (TPR) * (NV)) {                                                                             \
-        constexpr int rpb = (TPR) < 256 ? 256 / (TPR) : 1;                                                \
-        hipLaunchKernelGGL((norm_fwd_kernel<T, TPR, NV, OUT>), dim3((a.T + rpb - 1) / rpb),               \
-                           dim3((TPR) < 256 ? 256 : (TPR)), 0, s, a);                                     \
+        constexpr int rpb = 256 / (TPR);                                                                  \
+        const unsigned blocks = ((unsigned)a.T + rpb - 1) / rpb, x = blocks < most ? blocks : most;       \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, TPR, NV, OUT>), dim3(x, (blocks + x - 1) / x), dim3(256), 0, s, a); \
         return hipGetLastError();                                                                         \
     }
     MOE_NORM_LAUNCH(64, 1)

@@ -48,11 +48,10 @@ int check_rows(int M, int N, int K, int E, int T, int k)
     if (M < 0 || N <= 0 || K <= 0 || E <= 0 || T < 0 || k < 1) return MOE_ERR_INVALID_ARG;
     if (E > kMaxExperts || k > kMaxTopK || N > kMaxWidth || K > kMaxWidth) return MOE_ERR_UNSUPPORTED;
     if ((int64_t)E * N * K > (int64_t)1 << 37) return MOE_ERR_UNSUPPORTED;
-    // grid sizes, for the smallest tile (128 x 64); the bias gradient's rows of workgroups
-    const int64_t wide = (N > K ? N : K) / 64 + 1;
-    if (wide * ((int64_t)M / 64 + E + 1) > INT32_MAX - 16) return MOE_ERR_UNSUPPORTED;
-    if (M / 128 + E > (1 << 24)) return MOE_ERR_UNSUPPORTED;
-    if (((int64_t)N / 64 + 1) * ((int64_t)K / 128 + 2) * E * 64 > INT32_MAX - 16) return MOE_ERR_UNSUPPORTED;
+    // A launch holds fewer than 2^32 threads, 256 in a workgroup; tiles of 128 x 64.
+    const int64_t most = ((int64_t)1 << 24) - 16, wide = (N > K ? N : K) / 64 + 1;
+    if (wide * ((int64_t)M / 64 + E + 1) > most) return MOE_ERR_UNSUPPORTED;
+    if (((int64_t)N / 64 + 1) * ((int64_t)K / 128 + 2) * E > most) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 
@@ -124,6 +123,9 @@ int check_w4(const moe_w4* d)
     if (d->out_dtype != d->dtype && d->out_dtype != MOE_DT_F32) return MOE_ERR_UNSUPPORTED;
     if (d->act != MOE_ACT_NONE && d->act != MOE_ACT_SWIGLU) return MOE_ERR_UNSUPPORTED;
     if (d->act == MOE_ACT_SWIGLU && d->N % 2 != 0) return MOE_ERR_INVALID_ARG;
+    // work items are counted in 32 bits, whatever the offsets say
+    const int64_t passes = d->M <= 4 * d->E ? d->M / 4 + 1 : d->M / 16 + 1;
+    if (passes * d->E * ((int64_t)d->N / 32 + 1) > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

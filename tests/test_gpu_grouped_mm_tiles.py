@@ -86,3 +86,44 @@ def test_weight_gradient_tiles(name, dtype):
         moe.moe_grouped_mm_wgrad(d, _put(a), _put(off), _put(pairs), _put(dc), db2, None, ws, n)
         torch.cuda.synchronize()
         assert torch.equal(db, db2), "the same call gives other bits"
+
+
+def _guarded(*shape, dtype=torch.bfloat16):
+    """A zeroed buffer with 4096 bytes of 0xA5 before and behind it."""
+    n = torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size()
+    raw = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    raw[4096:4096 + n] = 0
+    return raw, raw[4096:4096 + n].view(dtype).view(shape)
+
+
+@pytest.mark.parametrize("M", [60, 3000])
+def test_offsets_that_decrease_stay_inside(M):
+    """Segments that overlap many times over hold more rows than there are: what
+    they give is unspecified, but nothing outside the buffers is touched, and
+    the next call is right."""
+    E, N, K = 9, 136, 64
+    a, b, bias, dc, _, _, _ = _case(35, "bf16", M, 1, E, N, K, False)
+    off = torch.tensor([0, M] * 5, dtype=torch.int32)
+    d, f = moe.gmm(M, N, K, E), moe.gmm(M, N, K, E, out_dtype=moe.MOE_DT_F32)
+    bufs = {"y": _guarded(M, N), "da": _guarded(M, K), "db": _guarded(E, N, K, dtype=torch.float32),
+            "dbias": _guarded(E, N, dtype=torch.float32),
+            "ws": _guarded(moe.moe_grouped_mm_workspace_size(f), dtype=torch.uint8), "q": _guarded(M, N)}
+    o = {n: t for n, (_, t) in bufs.items()}
+    codes = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((E, N, K // 32), 0.01, dtype=torch.bfloat16, device="cuda")
+    wd = moe.w4(M, N, K, E, group=32)
+    for offsets in (off, torch.linspace(0, M, E + 1).to(torch.int32)):
+        moe.moe_grouped_mm(d, a.cuda(), offsets.cuda(), None, b.cuda(), bias.cuda(), o["y"])
+        moe.moe_grouped_mm_dgrad(d, dc.cuda(), offsets.cuda(), b.cuda(), o["da"])
+        moe.moe_grouped_mm_wgrad(f, a.cuda(), offsets.cuda(), None, dc.cuda(), o["db"], o["dbias"], o["ws"], o["ws"].numel())
+        moe.moe_w4_matvec(wd, a.cuda(), offsets.cuda(), None, codes, scales, None, bias.cuda(), o["q"])
+        torch.cuda.synchronize()
+        for n, (raw, _) in bufs.items():
+            assert (raw[:4096] == 0xA5).all() and (raw[-4096:] == 0xA5).all(), f"{n}: written outside"
+    want, bound, _ = ref.product(a, offsets, None, 1, b, bias, torch.bfloat16, M)
+    ref.assert_within(o["y"], want, bound, "forward")
+    want, bound, wbias, bbias = ref.product_wgrad(a, offsets, None, 1, dc, E, torch.float32, M)
+    ref.assert_within(o["db"], want, bound, "wgrad")
+    ref.assert_within(o["dbias"], wbias, bbias, "dbias")
+    want, bound, _ = ref.w4_product(a, offsets, None, 1, codes.cpu(), scales.cpu(), None, bias, 32, False, torch.bfloat16, M)
+    ref.assert_within(o["q"], want, bound, "w4")
