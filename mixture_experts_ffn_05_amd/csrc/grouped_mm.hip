@@ -37,8 +37,8 @@
 //
 // Bound by the matrix cores at the clock that their load allows: 1116 us for
 // 32768 rows, 32 experts of Zipf shares, 2880 -> 5760 bf16 (0.97 PFLOP/s; the
-// library's dense product of those sizes 1.23), 1289 us for both gradients at
-// 2880 x 2880 (0.84 PFLOP/s; dense 1.11 and 0.73).  What each part gave: loads
+// library's dense product of those sizes 1.23), 1299 us for both gradients at
+// 2880 x 2880 with the bias gradient (0.84 PFLOP/s; dense 1.11 and 0.73).  What each part gave: loads
 // among the MFMAs 1201 -> 1125 us, no address arithmetic 1242 -> 1171.
 #include <string.h>
 
