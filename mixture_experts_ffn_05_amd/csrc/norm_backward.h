@@ -19,7 +19,9 @@
 // 2880 columns, those sums alone took 144 registers and spilled; four rows at
 // once needed over 200 and left one workgroup a CU: 197 us for the two kernels
 // on 8192 x 2880 bf16, against 106 us with one row and two workgroups.)
-// HBM bound: 3 rows moved per row.
+// HBM bound: 3 rows moved per row (4 with dres).  8192 x 2880 bf16: norm_in with
+// dres 35 us, 5.6 TB/s; norm_out with dropout and a channel gate 43 us, 3.6 TB/s,
+// where drawing the mask again and the sums take as long; column sums 4 us each.
 #pragma once
 
 #include <type_traits>

@@ -6,7 +6,8 @@
 // (layer), statistics in fp32 from the values held in registers: every row is
 // read once, whatever its kind (the layer norm's variance is the mean of the
 // squared differences from the mean, a second pass over registers).  Bound by
-// HBM: 2 rows moved per row of norm_in, 3 (4 with a full gate) of norm_out.
+// HBM: 2 rows moved per row of norm_in, 3 (4 with a full gate) of norm_out.  8192 x
+// 2880 bf16: 20.6 and 30.2 us, 4.6 and 4.7 TB/s (a copy reaches 4.9).
 //
 // A row is held by one wave up to 2048 columns (no barrier, rows independent, 4
 // of them in a workgroup), by 256 threads above, each thread keeping vectors of

