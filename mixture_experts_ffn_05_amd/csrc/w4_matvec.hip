@@ -99,9 +99,17 @@ struct WqShape {
     // 14.6 and 21.8 us (64 rows, 2880 -> 2880).
     static constexpr int CK = XR < 16 && KS == 1 ? 256 : 128, ROWB = CK / 2;
     static constexpr int BPC = CK / 32, GPC = BPC / GB;  // 32-column blocks, groups per chunk
-    static constexpr int WBYTES = 32 * ROWB, XBYTES = XR * 2 * CK, SBYTES = GPC < 2 ? 256 : 32 * GPC * 4;
-    static constexpr int SLOT = WBYTES + XBYTES + (Z ? 2 : 1) * SBYTES;
-    static constexpr int RING = WQ_NW * WQ_DEPTH * SLOT, RED = KS > 1 ? WQ_NW * 2 * WAVE : 1;
+    static constexpr int WBYTES = 32 * ROWB, XBYTES = XR * 2 * CK;
+    // Scales and zero points are gathered for SPAN chunks at once, into one of two
+    // tables (one slot's, where SPAN is 1): a gather's cost is the cache lines it
+    // touches, one a row.  Two chunks where the tables leave room for two
+    // workgroups a CU and a wave's chunks are adjacent.
+    static constexpr int table(int span) { return span * GPC < 2 ? 256 : 32 * span * GPC * 4; }
+    static constexpr int SPAN =
+        KS == 1 && WQ_NW * 2 * (WBYTES + XBYTES + (Z ? 2 : 1) * table(2)) + 16 <= 80 * 1024 ? 2 : 1;
+    static constexpr int SBYTES = table(SPAN), SLOT = WBYTES + XBYTES, TABLE = (Z ? 2 : 1) * SBYTES;
+    static constexpr int RING = WQ_NW * WQ_DEPTH * (SLOT + TABLE), RED = KS > 1 ? WQ_NW * 2 * WAVE : 1;
+    static_assert(WQ_DEPTH == 2, "a table per slot, or two chunks a table");
     // Two workgroups per CU where their LDS fits: asking for them also keeps
     // the matrix cores' results in ordinary registers.
     static constexpr int WAVES_PER_SIMD = RING + RED * 16 <= 80 * 1024 ? 2 : 1;
@@ -113,10 +121,11 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
     using S = WqShape<GB, Z, XR, KS>;
     static_assert(KS == 1 || KS == WQ_NW, "an item belongs to a wave or to a workgroup");
     constexpr int GPC = S::GPC, WBYTES = S::WBYTES, XBYTES = S::XBYTES, SBYTES = S::SBYTES, SLOT = S::SLOT;
+    constexpr int SPAN = S::SPAN, TG = SPAN * GPC;  // chunks, groups per table
     constexpr int WQ_CK = S::CK, WQ_ROWB = S::ROWB;
     constexpr int WL = WBYTES / 1024, XL = XBYTES / 1024, SL = SBYTES / 256;  // loads per slot
-    constexpr int NL = WL + XL + (Z ? 2 : 1) * SL;
-    static_assert(XL >= 1 && (WQ_DEPTH - 1) * NL < 64, "load count");
+    constexpr int NL = WL + XL, NT = (Z ? 2 : 1) * SL;  // of a slot, of a table
+    static_assert(XL >= 1 && NL + NT < 64, "load count");
     __shared__ __attribute__((aligned(16))) uint8_t sh[S::RING];
     __shared__ f32x4 red[S::RED];
 
@@ -124,9 +133,10 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
     const int l16 = lane & 15, kg = lane >> 4;
     const bool swiglu = g.swiglu;
     const int half = g.N / 2, G = (g.K + g.group - 1) / g.group;
-    const int nchunks = (g.K + WQ_CK - 1) / WQ_CK;
+    const int nchunks = (g.K + SPAN * WQ_CK - 1) / (SPAN * WQ_CK) * SPAN;  // whole tables; zeros past K
     const int tiles = swiglu ? (half + 15) / 16 : (g.N + 31) / 32;
-    uint8_t* ring = sh + wave * WQ_DEPTH * SLOT;
+    uint8_t* ring = sh + wave * WQ_DEPTH * (SLOT + S::TABLE);
+    uint8_t* tables = ring + WQ_DEPTH * SLOT;
     const int cw = KS > 1 ? wave : 0;  // first chunk of this wave
 
     // ---- every expert's segment, one per lane (E <= 256), and its first item
@@ -196,8 +206,8 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         }
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
-            const int q = min(lane + WAVE * i, 32 * GPC - 1);
-            const size_t at = (erow + wrow(t, q / GPC)) * G + q % GPC;
+            const int q = min(lane + WAVE * i, 32 * TG - 1);
+            const size_t at = (erow + wrow(t, q / TG)) * G + q % TG;
             ssrc[i] = reinterpret_cast<uintptr_t>(g.scales) + 2 * at;
             if (Z) zsrc[i] = reinterpret_cast<uintptr_t>(g.zeros) + at;
         }
@@ -222,6 +232,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         }
     };
     // Chunk c of the open item into a slot; chunks at or past nchunks read zeros only.
+    int itab = 0, ctab = 0;  // table to fill, table in use
     auto issue = [&](int c, int slot) {
         uint8_t* at = ring + slot * SLOT;
         const int k0 = c * WQ_CK;
@@ -233,14 +244,15 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
 #pragma unroll
         for (int i = 0; i < XL; ++i)
             dma16(reinterpret_cast<const void*>(k0 < xlim[i] ? xsrc[i] + 2 * (size_t)k0 : zeros), at + WBYTES + 1024 * i);
+        if (SPAN > 1 && slot) return;  // an even chunk brings the table of two
+        uint8_t* tab = tables + itab * S::TABLE;
+        itab ^= 1;
 #pragma unroll
         for (int i = 0; i < SL; ++i) {
-            const bool ok = c * GPC + min(lane + WAVE * i, 32 * GPC - 1) % GPC < G;
-            dma_u16(reinterpret_cast<const void*>(ok ? ssrc[i] + 2 * (size_t)(c * GPC) : zeros),
-                    at + WBYTES + XBYTES + 256 * i);
+            const bool ok = c * GPC + min(lane + WAVE * i, 32 * TG - 1) % TG < G;
+            dma_u16(reinterpret_cast<const void*>(ok ? ssrc[i] + 2 * (size_t)(c * GPC) : zeros), tab + 256 * i);
             if constexpr (Z)
-                dma_u8(reinterpret_cast<const void*>(ok ? zsrc[i] + (size_t)(c * GPC) : zeros),
-                       at + WBYTES + XBYTES + SBYTES + 256 * i);
+                dma_u8(reinterpret_cast<const void*>(ok ? zsrc[i] + (size_t)(c * GPC) : zeros), tab + SBYTES + 256 * i);
         }
     };
 
@@ -283,9 +295,14 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
         cur = locate(it);
         f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
         for (int c = cw; c < nchunks; c += KS) {
-            dma_wait<(WQ_DEPTH - 1) * NL>();
+            // all but the next chunk's loads, which have a table's among them unless
+            // this chunk's table is also the next one's
+            if (SPAN > 1 && slot == 0)
+                dma_wait<NL>();
+            else
+                dma_wait<NL + NT>();
             const uint8_t* at = ring + slot * SLOT;
-            const uint32_t* st = reinterpret_cast<const uint32_t*>(at + WBYTES + XBYTES);
+            const uint32_t* st = reinterpret_cast<const uint32_t*>(tables + ctab * S::TABLE) + (SPAN > 1 ? slot * GPC : 0);
 #pragma unroll
             for (int q = 0; q < GPC; q += SPC) {  // a set of groups
                 f32x4 dsum[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}, xsum = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -309,7 +326,7 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int si = (16 * n + l16) * GPC + q + d_slot;
+                    const int si = (16 * n + l16) * TG + q + d_slot;
                     const float sc = to_f32(T{(uint16_t)st[si]});
                     const float z = Z ? 16.f + (float)(st[SBYTES / 4 + si] & 15u) : 24.f;
 #pragma unroll
@@ -318,7 +335,8 @@ __global__ __launch_bounds__(WQ_THREADS, (WqShape<GB, Z, XR, KS>::WAVES_PER_SIMD
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this slot's reads are done
             advance(slot);
-            slot = slot + 1 == WQ_DEPTH ? 0 : slot + 1;
+            if (SPAN == 1 || slot) ctab ^= 1;
+            slot ^= 1;
         }
 
         // ---- the item's results: rows 4 kg % XR + i, summed over the slots
