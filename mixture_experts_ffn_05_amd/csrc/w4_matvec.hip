@@ -8,8 +8,9 @@
 // rows) times up to XR rows of x.  A wave streams its items' K in chunks of 256
 // (128) columns through its own ring of LDS slots, filled by direct-to-LDS loads
 // that run on into the next item: no barrier, no bubble between items, and
-// a slot's codes always in flight.  A slot holds 128 (64) bytes of each weight row, the chunk's scales and zero points and the
-// x rows' same columns, so nothing but LDS is read in the loop.  With few items
+// a slot's codes always in flight.  A slot holds 128 (64) bytes of each weight
+// row and the x rows' same columns, a table beside it the scales and zero points
+// of one or two chunks, so nothing but LDS is read in the loop.  With few items
 // (KS = 4) the 4 waves of a workgroup share an item, every fourth chunk each,
 // and add up through LDS.
 //
@@ -26,10 +27,11 @@
 // by side, so that one correction serves as many groups: the vector work per
 // code, not the matrix cores, is what competes with the memory here.
 //
-// 16 tokens, 4 of 128 experts, 2880 -> 5760 with SwiGLU, groups of 64: 118 us for
-// 463 MB (3.9 TB/s; 409 with slots filled through registers, 140 without the
-// groups side by side); vector instructions take half the cycles, the 2-byte
-// gathers of scales and zero points the rest of the gap to 75 us.
+// 16 tokens, 4 of 128 experts, 2880 -> 5760 with SwiGLU, groups of 64: 110 us for
+// 463 MB (4.2 TB/s; 409 with slots filled through registers, 140 without the
+// groups side by side, 117 with scales gathered for every chunk).  It is bound by
+// the cache lines that the loads touch: with 64-byte pieces of the rows, twice the
+// lines and the same bytes, it takes 150 us at two, three or four workgroups a CU.
 #include <string.h>
 
 #include <type_traits>
@@ -102,8 +104,9 @@ struct WqShape {
     static constexpr int WBYTES = 32 * ROWB, XBYTES = XR * 2 * CK;
     // Scales and zero points are gathered for SPAN chunks at once, into one of two
     // tables (one slot's, where SPAN is 1): a gather's cost is the cache lines it
-    // touches, one a row.  Two chunks where the tables leave room for two
-    // workgroups a CU and a wave's chunks are adjacent.
+    // touches, one a row.  Two chunks (110 us against 117 for one, 16 tokens as
+    // above) where the tables leave room for two workgroups a CU and a wave's
+    // chunks are adjacent.
     static constexpr int table(int span) { return span * GPC < 2 ? 256 : 32 * span * GPC * 4; }
     static constexpr int SPAN =
         KS == 1 && WQ_NW * 2 * (WBYTES + XBYTES + (Z ? 2 : 1) * table(2)) + 16 <= 80 * 1024 ? 2 : 1;
@@ -404,8 +407,8 @@ hipError_t launch_xr(const WqArgs& g, hipStream_t s)
     const long long items = tiles * ((g.M + XR - 1) / XR + (g.E == 1 ? 0 : g.E < g.M ? g.E : g.M));  // at most
     // A wave per item once there are items for every wave of the chip (two workgroups a CU),
     // a workgroup per item before.  Wave and workgroup, 2880 columns, in us: 1 row,
-    // 90 items 16 and 8, 1024 items 18 and 15, 2048 items 26 and 28; 32 experts'
-    // SwiGLU, 4 of them 17 and 13, 16 of them (2880 items) 32 and 35.
+    // 90 items 17 and 8, 1024 items 18 and 15, 2048 items 26 and 28; 32 experts'
+    // SwiGLU, 4 of them 18 and 13, 16 of them (3600 items) 34 and 36.
     if (items >= 8 * WQ_CUS) {
         const long long blocks = (items + WQ_NW - 1) / WQ_NW, most = 2 * WQ_CUS;
         hipLaunchKernelGGL((w4_matvec_kernel<T, GB, Z, XR, 1>), dim3((unsigned)(blocks < most ? blocks : most)),
@@ -419,8 +422,8 @@ hipError_t launch_xr(const WqArgs& g, hipStream_t s)
 // Rows of x per item: twice an expert's average share (its share varies), so
 // that a second pass over an expert's codes is rare, in the smallest form that
 // holds them; a wider one costs LDS space, and with it loads in flight.  32
-// experts' SwiGLU, 2880 -> 5760, in us: 2 rows each, 67 with 4 and 82 with 16; 4
-// rows each, 70, 72 and 85 with 4, 8 and 16; 8 rows each, 114 with 4 and 90 with 16.
+// experts' SwiGLU, 2880 -> 5760, in us: 2 rows each, 67 with 4 and 84 with 16; 4
+// rows each, 68, 71 and 84 with 4, 8 and 16; 8 rows each, 115 with 4 and 88 with 16.
 template <typename T, int GB, bool Z>
 hipError_t launch_rows(const WqArgs& g, hipStream_t s)
 {
